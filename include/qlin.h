@@ -301,6 +301,137 @@ QLIN_API qlin_status qlin_backward_dx_workspace(int32_t M, const qlin_weights* w
 QLIN_API qlin_status qlin_backward_dx(const qlin_weights* w, const uint16_t* dY, int32_t M, const float* s,
                                       uint16_t* dX, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- Layers with a fused epilogue, the gated block, and the norm in front
+ * of them: the feed-forward half of a transformer block,
+ *     y = x + W_down . (act(W_gate . n(x)) * (W_up . n(x))),
+ * for serving (one token and up) and for fine-tuning over frozen weights.
+ * Vectors along the channels (bias, gamma, beta and their gradients) and the
+ * row statistics are fp32. */
+typedef enum {
+  QLIN_ACT_NONE = 0,      /* z */
+  QLIN_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0 */
+  QLIN_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution function */
+  QLIN_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  QLIN_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} qlin_act;
+
+typedef enum {
+  QLIN_NORM_LAYER = 0,    /* subtracts the row's mean */
+  QLIN_NORM_RMS = 1       /* does not */
+} qlin_norm;
+
+/* The layer with bias, activation and residual in the GEMM's epilogue:
+ *   Z[m][n] = a_m * ( c'_n * acc[m][n] + comp[m][n] ) + bias[n]
+ *   Y[m][n] = fp16( act(Z[m][n]) + residual[m][n] )
+ * with a, acc and comp of qlin_forward; everything after acc is fp32 and Y
+ * is rounded once.  Without bias, activation and residual Y is qlin_forward's,
+ * bit for bit.
+ *   act       qlin_act.
+ *   bias      device fp32 [N], or NULL.
+ *   residual  device fp16 [M][N], or NULL.  Y may be the same buffer (the
+ *             residual stream updated in place).
+ *   Z         device fp16 [M][N] receiving the pre-activation rounded once
+ *             (for qlin_backward_act), or NULL.
+ *   X, s, gamma, update_momentum, workspace  as in qlin_forward; the size is
+ *             qlin_forward_act_workspace's.
+ * Apart from Y and residual no two buffers overlap. */
+QLIN_API qlin_status qlin_forward_act_workspace(int32_t M, const qlin_weights* w, size_t* bytes);
+QLIN_API qlin_status qlin_forward_act(const uint16_t* X, int32_t M, const qlin_weights* w, float* s, float gamma,
+                                      int32_t update_momentum, int32_t act, const float* bias,
+                                      const uint16_t* residual, uint16_t* Z, uint16_t* Y, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/* Its backward pass (straight-through estimator, as qlin_backward_dx):
+ *   dZ[m][n] = dY[m][n] * act'(Z[m][n])
+ *   dX       = dZ . Weff^T  (Weff of qlin_backward_dx)
+ *   dbias[n] = sum_m dZ[m][n]
+ * and the residual's gradient is dY itself.
+ *   Z      the forward's pre-activation; may be NULL when act is QLIN_ACT_NONE.
+ *   dX     device fp16 [M][K], fully overwritten, or NULL; dbias device fp32
+ *          [N], fully overwritten, or NULL; at least one of them is wanted.
+ *   s      as in qlin_backward_dx.
+ *   workspace  qlin_backward_act_workspace bytes, 256-byte aligned; it must
+ *          be zero-filled before its first use and is left that way where it
+ *          has to be.
+ * Arithmetic: dZ is formed in fp32 and rounded to fp16 once, multiplied by
+ * the mantissa of c'_n and by a power of two of its row that keeps it in
+ * range whatever the gradients' scale; the outlier rows of Weff are rounded
+ * to fp16, the other operand is exact; products are summed in fp32 and dX is
+ * rounded once.  dbias sums the fp32 dZ in an order fixed by the shape.
+ * M = 0 writes zeros to dbias; M above 65535 * 128 returns QLIN_ERR_SHAPE. */
+QLIN_API qlin_status qlin_backward_act_workspace(int32_t M, const qlin_weights* w, size_t* bytes);
+QLIN_API qlin_status qlin_backward_act(const qlin_weights* w, const uint16_t* dY, const uint16_t* Z, int32_t act,
+                                       int32_t M, const float* s, uint16_t* dX, float* dbias, void* workspace,
+                                       size_t ws_bytes, void* stream);
+
+/* Pack the gate and up projections of a gated block as one layer of N = 2 F
+ * channels: channel 2j is gate channel j, channel 2j + 1 up channel j, so
+ * both values of a product meet in one epilogue.  One outlier set and one
+ * momentum state serve both projections (they read the same input); the
+ * weight side of beta is the larger of the two.
+ *   W_gate, W_up  device fp16 [K][F] each; w is bound with N = 2 F (F % 8 == 0).
+ * Otherwise as qlin_pack_weights. */
+QLIN_API qlin_status qlin_pack_gated(const uint16_t* W_gate, const uint16_t* W_up, const int32_t* O_host,
+                                     const qlin_weights* w, void* stream);
+
+/* The gated block's first half in one GEMM: both projections, the activation
+ * and the product,
+ *   Z[m][n] = a_m * ( c'_n * acc[m][n] + comp[m][n] ) + bias[n]     (n < 2 F, gate and up alternating)
+ *   H[m][j] = fp16( act(Z[m][2j]) * Z[m][2j + 1] ),
+ * in fp32 up to the one rounding of H.
+ *   w     packed by qlin_pack_gated.
+ *   bias  device fp32 [2 F] in the packed order, or NULL.
+ *   Z     device fp16 [M][2 F] in the packed order receiving both
+ *         pre-activations (for qlin_backward_gated), or NULL.
+ *   H     device fp16 [M][F].
+ * The other arguments as in qlin_forward_act. */
+QLIN_API qlin_status qlin_forward_gated_workspace(int32_t M, const qlin_weights* w, size_t* bytes);
+QLIN_API qlin_status qlin_forward_gated(const uint16_t* X, int32_t M, const qlin_weights* w, float* s, float gamma,
+                                        int32_t update_momentum, int32_t act, const float* bias, uint16_t* Z,
+                                        uint16_t* H, void* workspace, size_t ws_bytes, void* stream);
+
+/* Its backward pass:
+ *   dZ[m][2j]     = dH[m][j] * Z[m][2j + 1] * act'(Z[m][2j])
+ *   dZ[m][2j + 1] = dH[m][j] * act(Z[m][2j])
+ *   dX = dZ . Weff^T,  dbias[n] = sum_m dZ[m][n]   (fp32 [2 F], packed order)
+ * with the arithmetic and arguments of qlin_backward_act (Z is required). */
+QLIN_API qlin_status qlin_backward_gated_workspace(int32_t M, const qlin_weights* w, size_t* bytes);
+QLIN_API qlin_status qlin_backward_gated(const qlin_weights* w, const uint16_t* dH, const uint16_t* Z, int32_t act,
+                                         int32_t M, const float* s, uint16_t* dX, float* dbias, void* workspace,
+                                         size_t ws_bytes, void* stream);
+
+/* Layer norm or RMS norm of token rows (what a quantized layer reads):
+ *   mu_m = mean_k X[m][k] (0 for RMS),  r_m = 1 / sqrt(mean_k (X[m][k] - mu_m)^2 + eps)
+ *   Y[m][k] = fp16( (X[m][k] - mu_m) r_m gamma[k] + beta[k] )
+ * in fp32, the squares summed after the mean is subtracted.
+ *   kind   qlin_norm.
+ *   gamma  device fp32 [K]; beta device fp32 [K] or NULL.
+ *   eps    > 0.
+ *   Y      device fp16 [M][K]; may be X.
+ *   mean, rstd  device fp32 [M] receiving mu and r (for the backward pass), or
+ *          NULL; the RMS norm does not write mean.
+ * K % 32 == 0, K <= 65536.  M may be 0. */
+QLIN_API qlin_status qlin_norm_forward(const uint16_t* X, int32_t M, int32_t K, int32_t kind, const float* gamma,
+                                       const float* beta, float eps, uint16_t* Y, float* mean, float* rstd,
+                                       void* stream);
+
+/* Its backward pass, with xh = (X - mu) r and w = dY gamma:
+ *   dX     = fp16( r ( w - mean_k w - xh mean_k(w xh) ) + dres )   (no mean_k w for RMS)
+ *   dgamma = sum_m dY xh,   dbeta = sum_m dY    (fp32, in an order fixed by the shape)
+ *   mean, rstd  the forward's (mean is not read for RMS and may be NULL).
+ *   dres   device fp16 [M][K], or NULL: the gradient that reaches X beside
+ *          the norm (a residual stream's).
+ *   dX     device fp16 [M][K] or NULL; may be the buffer of dY, X or dres.
+ *   dgamma, dbeta  device fp32 [K] or NULL; at least one output is wanted.
+ *   workspace  qlin_norm_backward_workspace bytes, 256-byte aligned, needed
+ *          when dgamma or dbeta is wanted; no zero-fill needed.
+ * M = 0 writes zeros to dgamma and dbeta. */
+QLIN_API qlin_status qlin_norm_backward_workspace(int32_t M, int32_t K, size_t* bytes);
+QLIN_API qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M, int32_t K, int32_t kind,
+                                        const float* gamma, const float* mean, const float* rstd,
+                                        const uint16_t* dres, uint16_t* dX, float* dgamma, float* dbeta,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
 /* Hessian-compensated quantization of a layer's weights (offline, before
  * packing; "QQQ: Quality Quattuor-Bit Quantization for Large Language
  * Models", section 三 技术架构 -> Hessian补偿): with H = 2 X^T X over the

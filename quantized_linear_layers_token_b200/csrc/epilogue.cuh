@@ -1,0 +1,121 @@
+// epilogue.cuh -- what the fused linear layers compute on each pre-activation
+// value: bias, activation, residual, the gated product, and the activation's
+// derivative for the backward pass.
+//
+//   relu(z) = max(z, 0)                 relu'  = [z > 0]
+//   gelu(z) = z Phi(z)                  gelu'  = Phi(z) + z phi(z)
+//   gelu_tanh(z) = z p, p = 1 / (1 + exp(-2 u)), u = sqrt(2/pi) (z + 0.044715 z^3)
+//                                       slope  = p + z p (1 - p) 2 u'
+//   silu(z) = z p, p = 1 / (1 + exp(-z))       = p (1 + z (1 - p))
+// with 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)).  All in fp32; the exponential
+// and the quotient are the hardware approximations (a few units of 2^-22,
+// far below half a step of the fp16 results), which reach 0 and z at the
+// ends of the range without an overflow: exp(-2 u) = inf gives p = 0.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace qlin {
+
+enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+// Epilogue variants of the GEMM kernels (template parameter).
+enum : int {
+  kEpiPlain = 0,  // Y = fp16(a (c' acc + comp))
+  kEpiAct = 1,    // Z = a (c' acc + comp) + bias; Y = act(Z) + residual
+  kEpiGated = 2   // the same Z; channels 2j, 2j + 1 are gate and up: Y[:, j] = act(Z[:, 2j]) Z[:, 2j + 1]
+};
+
+struct EpiArgs {
+  const float* bias;         // [N] or null
+  const uint16_t* residual;  // [M][N] or null (kEpiAct)
+  uint16_t* Z;               // [M][N] or null: the pre-activation, kept for the backward pass
+  int act;
+};
+
+__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+constexpr float kGeluTanhA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluTanhB = 0.044715f;
+
+// act(z) of N values, the choice made once.
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&z)[N]) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = z[i] * normcdff(z[i]);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = z[i] * sigmoid_f(kGeluTanhA * fmaf(kGeluTanhB * z[i], z[i] * z[i], z[i]));
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = z[i] * sigmoid_f(z[i]);
+      break;
+    default: break;
+  }
+}
+
+// act(z) and act'(z).
+__device__ __forceinline__ void act_slope(int act, float z, float& value, float& slope) {
+  switch (act) {
+    case kActRelu:
+      value = z < 0.f ? 0.f : z;
+      slope = z > 0.f ? 1.f : 0.f;
+      break;
+    case kActGelu: {
+      const float p = normcdff(z);
+      value = z * p;
+      slope = fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), p);
+      break;
+    }
+    case kActGeluTanh: {
+      const float z2 = z * z;
+      const float p = sigmoid_f(kGeluTanhA * fmaf(kGeluTanhB * z, z2, z));
+      value = z * p;
+      slope = fmaf(z * p * (1.f - p), kGeluTanhA * fmaf(3.f * kGeluTanhB, z2, 1.f), p);
+      break;
+    }
+    case kActSilu: {
+      const float p = sigmoid_f(z);
+      value = z * p;
+      slope = p * fmaf(z, 1.f - p, 1.f);
+      break;
+    }
+    default:
+      value = z;
+      slope = 1.f;
+  }
+}
+
+// Gated product of a channel pair held by two neighbouring lanes: the even
+// lane holds the gate's, the odd lane the up projection's pre-activations of
+// 2 n tokens.  After one exchange the even lane has both values of the first
+// n tokens and the odd lane those of the last n; h[i] is act(gate) * up of
+// token i (even lane) or n + i (odd lane).  `mask` names the lanes that call
+// together (at least the pair).
+template <int N2>
+__device__ __forceinline__ void gated_pair(int act, const float (&z)[N2], bool odd, unsigned mask, float (&h)[N2 / 2]) {
+  constexpr int n = N2 / 2;
+  float up[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const float send = odd ? z[i] : z[n + i];
+    const float keep = odd ? z[n + i] : z[i];
+    const float got = __shfl_xor_sync(mask, send, 1);
+    h[i] = odd ? got : keep;
+    up[i] = odd ? keep : got;
+  }
+  act_values<n>(act, h);
+#pragma unroll
+  for (int i = 0; i < n; ++i) h[i] *= up[i];
+}
+
+}  // namespace qlin

@@ -46,9 +46,12 @@
 // Epilogue (Quaff notes, decoupled WAQ formula; QQQ review, fused INT32->FP16
 // dequant): Y = fp16(a_m * (c'_n * acc + comp)), comp accumulated in fp32 on
 // the tensor cores from W_O^T and U = XqO * (s - 1) carried as two fp16
-// terms (hi and lo) into the same accumulator.
+// terms (hi and lo) into the same accumulator.  The fused layers (EPI, one
+// problem per launch) go on in fp32 from a_m * (c'_n * acc + comp): bias,
+// activation, residual, or the gated product of neighbouring channels.
 #pragma once
 
+#include "epilogue.cuh"
 #include "sm100.cuh"
 
 namespace qlin {
@@ -148,6 +151,7 @@ struct GemmArgs {
   // 1: the weight blocks were written by the previous kernel (INT4 widened
   // once per call), so the weight producer waits on the grid dependency too
   int wdep;
+  EpiArgs epi;  // fused epilogues (EPI != kEpiPlain; one problem per launch)
   // bnd[c] = first iteration of CTA c, bnd[grid] = total (computed on the
   // host by gemm_boundaries(); kernel parameters, read from the constant
   // cache).
@@ -524,12 +528,159 @@ widen_w4_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ 
   }
 }
 
-template <int FMT, int BT, int MAXP>
+// ---- fused epilogues.  Three forms, one for each way a finished value
+// reaches the epilogue threads; all of them go on in fp32 and round each
+// output once.
+
+// A whole tile's chunk of 16 tokens, thread = channel: z[j] is the value of
+// token c0 + j before the bias.  `ys` are the group's two staging buffers,
+// which alternate (`ycnt`): one barrier between the writes of a buffer and
+// its reads suffices, and the next write of the same buffer comes after the
+// barrier of the other.
+template <int EPI, int BT>
+__device__ __forceinline__ void epi_whole(const EpiArgs& e, const GemmProb& pr, float (&z)[16], float bias_n, int tn,
+                                          int nl, int m0, int c0, int mvalid, int gbar, uint16_t* ys, int& ycnt) {
+  const int n = tn * 128 + nl;
+  uint16_t res[16];
+  if (EPI == kEpiAct && e.residual) {
+    // a warp reads 32 neighbouring channels of one token: two full sectors
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      res[j] = (c0 + j < mvalid && n < pr.N) ? e.residual[static_cast<size_t>(m0 + c0 + j) * pr.N + n] : uint16_t(0);
+  }
+  if (e.bias) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) z[j] = __fadd_rn(z[j], bias_n);
+  }
+  if (e.Z) {
+    uint16_t* st = ys + (ycnt & 1) * 2048;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) st[j * 128 + nl] = __half_as_ushort(__float2half_rn(z[j]));
+    named_bar_sync(gbar, 128);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int idx = nl + h * 128;
+      const int j = idx >> 4;
+      const int n8 = tn * 128 + (idx & 15) * 8;
+      if (c0 + j < mvalid && n8 < pr.N)
+        *reinterpret_cast<uint4*>(e.Z + static_cast<size_t>(m0 + c0 + j) * pr.N + n8) =
+            *reinterpret_cast<const uint4*>(st + j * 128 + (idx & 15) * 8);
+    }
+    ++ycnt;
+  }
+  uint16_t* st = ys + (ycnt & 1) * 2048;
+  if (EPI == kEpiGated) {
+    const bool odd = nl & 1;
+    float h[8];
+    gated_pair<16>(e.act, z, odd, 0xffffffffu, h);
+    const int t0 = odd ? 8 : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st[(t0 + i) * 64 + (nl >> 1)] = __half_as_ushort(__float2half_rn(h[i]));
+    named_bar_sync(gbar, 128);
+    const int j = nl >> 3;  // 16 rows x 8 segments of 8 channels
+    const int F = pr.N >> 1;
+    const int f8 = tn * 64 + (nl & 7) * 8;
+    if (c0 + j < mvalid && f8 < F)
+      *reinterpret_cast<uint4*>(pr.Y + static_cast<size_t>(m0 + c0 + j) * F + f8) =
+          *reinterpret_cast<const uint4*>(st + j * 64 + (nl & 7) * 8);
+  } else {
+    act_values<16>(e.act, z);
+    if (e.residual) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) z[j] = __fadd_rn(z[j], __half2float(__ushort_as_half(res[j])));
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) st[j * 128 + nl] = __half_as_ushort(__float2half_rn(z[j]));
+    named_bar_sync(gbar, 128);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int idx = nl + h * 128;
+      const int j = idx >> 4;
+      const int n8 = tn * 128 + (idx & 15) * 8;
+      if (c0 + j < mvalid && n8 < pr.N)
+        *reinterpret_cast<uint4*>(pr.Y + static_cast<size_t>(m0 + c0 + j) * pr.N + n8) =
+            *reinterpret_cast<const uint4*>(st + j * 128 + (idx & 15) * 8);
+    }
+  }
+  ++ycnt;
+}
+
+// Cluster split-K owner: four tokens from row m of channel n, the bias
+// already added; the first `valid` of them exist.  Neighbouring lanes hold
+// neighbouring channels of the same tokens.
+template <int EPI>
+__device__ __forceinline__ void epi_quad(const EpiArgs& e, const GemmProb& pr, float (&z)[4], int n, int m, int valid) {
+  const bool in = n < pr.N;  // N is even: both channels of a pair or neither
+  if (e.Z) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (in && i < valid) e.Z[static_cast<size_t>(m + i) * pr.N + n] = __half_as_ushort(__float2half_rn(z[i]));
+  }
+  if (EPI == kEpiGated) {
+    const bool odd = n & 1;
+    float h[2];
+    gated_pair<4>(e.act, z, odd, 3u << (threadIdx.x & 30), h);
+    const int t0 = odd ? 2 : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (in && t0 + i < valid)
+        pr.Y[static_cast<size_t>(m + t0 + i) * (pr.N >> 1) + (n >> 1)] = __half_as_ushort(__float2half_rn(h[i]));
+  } else {
+    uint16_t res[4] = {0, 0, 0, 0};
+    if (e.residual) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (in && i < valid) res[i] = e.residual[static_cast<size_t>(m + i) * pr.N + n];
+    }
+    act_values<4>(e.act, z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e.residual) z[i] = __fadd_rn(z[i], __half2float(__ushort_as_half(res[i])));
+      if (in && i < valid) pr.Y[static_cast<size_t>(m + i) * pr.N + n] = __half_as_ushort(__float2half_rn(z[i]));
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  return static_cast<uint32_t>(__half_as_ushort(__float2half_rn(a))) |
+         (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(b))) << 16);
+}
+
+// Stream-K finisher: channels n4 .. n4 + 3 of token row m, before the bias.
+template <int EPI>
+__device__ __forceinline__ void epi_row4(const EpiArgs& e, uint16_t* Y, float (&z)[4], const float (&b4)[4], int n4,
+                                         size_t m, int N) {
+  if (e.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = __fadd_rn(z[i], b4[i]);
+  }
+  if (e.Z) *reinterpret_cast<uint2*>(e.Z + m * N + n4) = make_uint2(pack_h2(z[0], z[1]), pack_h2(z[2], z[3]));
+  if (EPI == kEpiGated) {
+    float h[2] = {z[0], z[2]};
+    act_values<2>(e.act, h);
+    *reinterpret_cast<uint32_t*>(Y + m * (N >> 1) + (n4 >> 1)) = pack_h2(h[0] * z[1], h[1] * z[3]);
+  } else {
+    uint2 r = make_uint2(0u, 0u);
+    if (e.residual) r = *reinterpret_cast<const uint2*>(e.residual + m * N + n4);
+    act_values<4>(e.act, z);
+    if (e.residual) {
+      const float2 r0 = __half22float2(u32_as_h2(r.x)), r1 = __half22float2(u32_as_h2(r.y));
+      z[0] = __fadd_rn(z[0], r0.x);
+      z[1] = __fadd_rn(z[1], r0.y);
+      z[2] = __fadd_rn(z[2], r1.x);
+      z[3] = __fadd_rn(z[3], r1.y);
+    }
+    *reinterpret_cast<uint2*>(Y + m * N + n4) = make_uint2(pack_h2(z[0], z[1]), pack_h2(z[2], z[3]));
+  }
+}
+
+template <int FMT, int BT, int MAXP, int EPI>
 __global__ void __launch_bounds__(GemmCfg<FMT, BT>::kThreads, 1)
 gemm_kernel(const __grid_constant__ GemmParams<MAXP> prm) {
   using C = GemmCfg<FMT, BT>;
   const GemmArgs& args = prm.g;
   const GemmProb* const probs = prm.pr;
+  static_assert(EPI == kEpiPlain || MAXP == 1, "fused epilogues take one problem per launch");
   const int nprob = MAXP == 1 ? 1 : args.nprob;
   constexpr int P = C::kASlots;
   constexpr int XS = C::kXSlots;
@@ -1167,6 +1318,13 @@ gemm_kernel(const __grid_constant__ GemmParams<MAXP> prm) {
         const bool has_comp = pcomp && sg.r1 == pr.T && sg.r0 <= pr.nk;
         const bool whole = sg.r0 == 0 && sg.r1 == pr.T;
         const float cn = chan_scale<FMT>(pr, n);
+        // fused epilogues: this channel's bias (cluster split-K: the owned
+        // channel's); adding -0 changes no value
+        float bias_n = -0.f;
+        if (EPI != kEpiPlain && args.epi.bias) {
+          const int nb = cl ? tn * C::kBN + crk * slice + (nl % slice) : n;
+          if (nb < pr.N) bias_n = __ldg(args.epi.bias + nb);
+        }
         float a_own = 0.f, cn_own = 0.f;  // cluster split-K: the owned slice's scales
         if (cl) {
           cn_own = chan_scale<FMT>(pr, tn * C::kBN + crk * slice + (nl % slice));
@@ -1251,31 +1409,39 @@ gemm_kernel(const __grid_constant__ GemmParams<MAXP> prm) {
               sc[4 * q4] = t.x; sc[4 * q4 + 1] = t.y; sc[4 * q4 + 2] = t.z; sc[4 * q4 + 3] = t.w;
             }
             uint16_t yh[16];
+            float z[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               float v = __fmul_rn(cn, static_cast<float>(static_cast<int32_t>(acc[j])));
               if (pcomp) v = __fadd_rn(v, __uint_as_float(cmp[j]));
-              yh[j] = __half_as_ushort(__float2half_rn(__fmul_rn(sc[j], v)));
+              z[j] = __fmul_rn(sc[j], v);
             }
+            if constexpr (EPI != kEpiPlain) {
+              epi_whole<EPI, BT>(args.epi, pr, z, bias_n, tn, nl, m0, c0, mvalid, gbar,
+                                 reinterpret_cast<uint16_t*>(smem + C::kOffYst + grp * 2 * C::kYStage), ycnt);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) ys[j * 128 + nl] = yh[j];
-            if (pr.acc_debug) {
-              for (int j = 0; j < 16; ++j)
-                if (c0 + j < mvalid && n < pr.N)
-                  pr.acc_debug[static_cast<size_t>(m0 + c0 + j) * pr.N + n] = static_cast<int32_t>(acc[j]);
-            }
-            named_bar_sync(gbar, 128);
+              for (int j = 0; j < 16; ++j) yh[j] = __half_as_ushort(__float2half_rn(z[j]));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int idx = nl + h * 128;  // 16 rows x 16 segments of 8 channels
-              const int j = idx >> 4;
-              const int n8 = tn * C::kBN + (idx & 15) * 8;
-              if (c0 + j < mvalid && n8 < pr.N)
-                *reinterpret_cast<uint4*>(pr.Y + static_cast<size_t>(m0 + c0 + j) * pr.N + n8) =
-                    *reinterpret_cast<const uint4*>(ys + j * 128 + (idx & 15) * 8);
+              for (int j = 0; j < 16; ++j) ys[j * 128 + nl] = yh[j];
+              if (pr.acc_debug) {
+                for (int j = 0; j < 16; ++j)
+                  if (c0 + j < mvalid && n < pr.N)
+                    pr.acc_debug[static_cast<size_t>(m0 + c0 + j) * pr.N + n] = static_cast<int32_t>(acc[j]);
+              }
+              named_bar_sync(gbar, 128);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int idx = nl + h * 128;  // 16 rows x 16 segments of 8 channels
+                const int j = idx >> 4;
+                const int n8 = tn * C::kBN + (idx & 15) * 8;
+                if (c0 + j < mvalid && n8 < pr.N)
+                  *reinterpret_cast<uint4*>(pr.Y + static_cast<size_t>(m0 + c0 + j) * pr.N + n8) =
+                      *reinterpret_cast<const uint4*>(ys + j * 128 + (idx & 15) * 8);
+              }
+              if (seg == 0 && nl == 0 && c0 == 0) QLIN_STAMP(17);
+              ++ycnt;
             }
-            if (seg == 0 && nl == 0 && c0 == 0) QLIN_STAMP(17);
-            ++ycnt;
           } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -1336,15 +1502,26 @@ gemm_kernel(const __grid_constant__ GemmParams<MAXP> prm) {
               if (jq >= BT / 4) break;
               const int s4[4] = {sum[k].x, sum[k].y, sum[k].z, sum[k].w};
               const float p4[4] = {cp[k].x, cp[k].y, cp[k].z, cp[k].w};
+              if constexpr (EPI != kEpiPlain) {
+                float z[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int j = 4 * jq + i;
-                if (ok && j < mvalid && n_own < pr.N) {
+                for (int i = 0; i < 4; ++i) {
                   float v = __fmul_rn(cn_own, static_cast<float>(s4[i]));
                   if (pcomp) v = __fadd_rn(v, p4[i]);
-                  const float y = __fmul_rn(scl[k][i], v);
-                  pr.Y[static_cast<size_t>(m0 + j) * pr.N + n_own] = __half_as_ushort(__float2half_rn(y));
-                  if (pr.acc_debug) pr.acc_debug[static_cast<size_t>(m0 + j) * pr.N + n_own] = s4[i];
+                  z[i] = __fadd_rn(__fmul_rn(scl[k][i], v), bias_n);
+                }
+                epi_quad<EPI>(args.epi, pr, z, n_own, m0 + 4 * jq, ok ? mvalid - 4 * jq : 0);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int j = 4 * jq + i;
+                  if (ok && j < mvalid && n_own < pr.N) {
+                    float v = __fmul_rn(cn_own, static_cast<float>(s4[i]));
+                    if (pcomp) v = __fadd_rn(v, p4[i]);
+                    const float y = __fmul_rn(scl[k][i], v);
+                    pr.Y[static_cast<size_t>(m0 + j) * pr.N + n_own] = __half_as_ushort(__float2half_rn(y));
+                    if (pr.acc_debug) pr.acc_debug[static_cast<size_t>(m0 + j) * pr.N + n_own] = s4[i];
+                  }
                 }
               }
             }
@@ -1411,6 +1588,11 @@ gemm_kernel(const __grid_constant__ GemmParams<MAXP> prm) {
           float c4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) c4[i] = chan_scale<FMT>(pr, n4 + i);
+          float b4[4] = {0.f, 0.f, 0.f, 0.f};  // fused epilogues: the bias of the four channels
+          if (EPI != kEpiPlain && args.epi.bias && live) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(args.epi.bias + n4));
+            b4[0] = b.x; b4[1] = b.y; b4[2] = b.z; b4[3] = b.w;
+          }
           int nctr = 0;
           for (int c = c_lo; c <= c_hi; ++c) nctr += bnd_s(c, sbnd, args) != bnd_s(c + 1, sbnd, args) ? 1 : 0;
           const int blocks = nctr + (pcomp ? 1 : 0);
@@ -1474,7 +1656,9 @@ gemm_kernel(const __grid_constant__ GemmParams<MAXP> prm) {
                   if (pcomp) v = __fadd_rn(v, p4[e]);
                   y[e] = __fmul_rn(am, v);
                 }
-                if (live) {
+                if constexpr (EPI != kEpiPlain) {
+                  if (live) epi_row4<EPI>(args.epi, Yp, y, b4, n4, static_cast<size_t>(m0 + j0 + j), pr.N);
+                } else if (live) {
                   uint2 hv;
                   hv.x = static_cast<uint32_t>(__half_as_ushort(__float2half_rn(y[0]))) |
                          (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(y[1]))) << 16);

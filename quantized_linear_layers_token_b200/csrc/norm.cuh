@@ -1,0 +1,258 @@
+// norm.cuh -- layer norm and RMS norm in front of the quantized linear
+// layer: forward, and backward with the reduction of the weight's and the
+// bias's gradients over the tokens.
+//
+//   mu_m = mean_k x[m][k] (0 for RMS),  r_m = 1 / sqrt(mean_k (x - mu)^2 + eps)
+//   xh   = (x - mu_m) r_m,              y = xh gamma_k + beta_k
+//   dx   = r_m (w - mean_k w - xh mean_k(w xh)) + dres,  w = dy gamma_k
+//          (without the mean_k w term for RMS)
+//   dgamma_k = sum_m dy xh,             dbeta_k = sum_m dy
+//
+// Everything between the fp16 inputs and outputs is fp32: the statistics are
+// taken in two passes over the row held on chip (the sum of squares of
+// x - mu, not of x, so a large mean costs no digits), and each output is
+// rounded once.  Sums are added in an order that depends on the shape alone,
+// so results repeat bit for bit.
+#pragma once
+
+#include "pack.cuh"
+
+namespace qlin {
+
+constexpr int kNormMaxVec = 8192;  // 8-element vectors of a row (K <= 65536)
+
+struct NormFwdArgs {
+  const uint16_t* X;   // [M][K]
+  const float* gamma;  // [K]
+  const float* beta;   // [K] or null
+  uint16_t* Y;         // [M][K]
+  float* mean;         // [M] or null
+  float* rstd;         // [M] or null
+  int M, K, rms;
+  float eps;
+};
+
+struct NormBwdArgs {
+  const uint16_t* dY;    // [M][K]
+  const uint16_t* X;     // [M][K]
+  const float* gamma;    // [K]
+  const float* mean;     // [M], null for RMS
+  const float* rstd;     // [M]
+  const uint16_t* dres;  // [M][K] or null
+  uint16_t* dX;          // [M][K]
+  float* part;           // partial column sums: [G][K] of dgamma, then [G][K] of dbeta; null when none is wanted
+  int M, K, rms, G;
+};
+
+__device__ __forceinline__ void h8_to_f(const uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&w[e]);
+    const float2 t = __half22float2(h);
+    f[2 * e] = t.x;
+    f[2 * e + 1] = t.y;
+  }
+}
+__device__ __forceinline__ uint4 f_to_h8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 h = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void load_f8(const float* p, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over the T threads of a row.  `red` holds T / 32 floats and is free
+// again only after the next barrier: callers alternate two of them.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if (T == 32) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) s += red[w];
+  return s;
+}
+
+// Forward.  T threads share a row (four rows per CTA when T is one warp);
+// thread t holds the 8-element vectors t, t + T, ... of the row in
+// registers, VPT of them at most.
+template <int T, int VPT>
+__global__ void __launch_bounds__(T == 32 ? 128 : T) norm_forward_kernel(const __grid_constant__ NormFwdArgs g) {
+  __shared__ float red[2][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int t = T == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  const int m = T == 32 ? static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5) : static_cast<int>(blockIdx.x);
+  if (m >= g.M) return;  // whole warps (T = 32) or nobody
+  const int nv = g.K >> 3;
+  const uint4* xr = reinterpret_cast<const uint4*>(g.X + static_cast<size_t>(m) * g.K);
+  uint4 x[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = t + j * T;
+    x[j] = v < nv ? __ldg(xr + v) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  const float invk = 1.f / static_cast<float>(g.K);
+  float mu = 0.f;
+  if (!g.rms) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float f[8];
+      h8_to_f(x[j], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += f[e];
+    }
+    mu = row_sum<T>(s, red[0]) * invk;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    if (t + j * T < nv) {
+      float f[8];
+      h8_to_f(x[j], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q = fmaf(f[e] - mu, f[e] - mu, q);
+    }
+  }
+  const float r = 1.f / sqrtf(fmaf(row_sum<T>(q, red[1]), invk, g.eps));
+  uint4* yr = reinterpret_cast<uint4*>(g.Y + static_cast<size_t>(m) * g.K);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = t + j * T;
+    if (v < nv) {
+      float f[8], gm[8], bt[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      h8_to_f(x[j], f);
+      load_f8(g.gamma + 8 * v, gm);
+      if (g.beta) load_f8(g.beta + 8 * v, bt);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mu) * r, gm[e], bt[e]);
+      yr[v] = f_to_h8(f);
+    }
+  }
+  if (t == 0) {
+    if (g.mean) g.mean[m] = mu;
+    if (g.rstd) g.rstd[m] = r;
+  }
+}
+
+// Column sums of dy xh and dy over a block of rows: thread t of CTA (x, y)
+// owns the 8 columns of vector 128 x + t and the rows y, y + G, ...
+__global__ void __launch_bounds__(128) norm_columns_kernel(const __grid_constant__ NormBwdArgs g) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int v = blockIdx.x * 128 + threadIdx.x;
+  if (v >= (g.K >> 3)) return;
+  float sg[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sb[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int m = blockIdx.y; m < g.M; m += g.G) {
+    const size_t o = static_cast<size_t>(m) * g.K;
+    float x[8], dy[8];
+    h8_to_f(__ldg(reinterpret_cast<const uint4*>(g.X + o) + v), x);
+    h8_to_f(__ldg(reinterpret_cast<const uint4*>(g.dY + o) + v), dy);
+    const float mu = g.rms ? 0.f : __ldg(g.mean + m), r = __ldg(g.rstd + m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      sg[e] = fmaf(dy[e], (x[e] - mu) * r, sg[e]);
+      sb[e] += dy[e];
+    }
+  }
+  float4* pg = reinterpret_cast<float4*>(g.part + static_cast<size_t>(blockIdx.y) * g.K) + 2 * v;
+  float4* pb = reinterpret_cast<float4*>(g.part + static_cast<size_t>(g.G + blockIdx.y) * g.K) + 2 * v;
+  pg[0] = make_float4(sg[0], sg[1], sg[2], sg[3]);
+  pg[1] = make_float4(sg[4], sg[5], sg[6], sg[7]);
+  pb[0] = make_float4(sb[0], sb[1], sb[2], sb[3]);
+  pb[1] = make_float4(sb[4], sb[5], sb[6], sb[7]);
+}
+
+// out[k] = sum over the G partial rows, in one order: eight warps take the
+// rows w, w + 8, ... of 32 columns, and their sums are added in order.
+// blockIdx.y selects dgamma (0) or dbeta (1).
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part, int G, int K,
+                                                         float* __restrict__ out0, float* __restrict__ out1) {
+  __shared__ float red[8][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  float* out = blockIdx.y ? out1 : out0;
+  if (!out) return;
+  const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int k = blockIdx.x * 32 + c;
+  const float* p = part + static_cast<size_t>(blockIdx.y) * G * K + k;
+  float s = 0.f;
+  if (k < K) {
+#pragma unroll 8
+    for (int i = w; i < G; i += 8) s += p[static_cast<size_t>(i) * K];
+  }
+  red[w][c] = s;
+  __syncthreads();
+  if (w == 0 && k < K) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += red[i][c];
+    out[k] = s;
+  }
+}
+
+// Input gradient, one CTA of T threads per row, the row read twice (the
+// second time from L2).  dX may be the buffer of dY, X or dres: each thread
+// writes only the vectors it has just read.
+template <int T>
+__global__ void __launch_bounds__(T) norm_rows_kernel(const __grid_constant__ NormBwdArgs g) {
+  __shared__ float red[2][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int m = static_cast<int>(blockIdx.x);
+  const int nv = g.K >> 3;
+  const size_t o = static_cast<size_t>(m) * g.K;
+  const uint4* xr = reinterpret_cast<const uint4*>(g.X + o);
+  const uint4* dr = reinterpret_cast<const uint4*>(g.dY + o);
+  const float mu = g.rms ? 0.f : g.mean[m], r = g.rstd[m];
+  float s1 = 0.f, s2 = 0.f;
+  for (int v = threadIdx.x; v < nv; v += T) {
+    float x[8], dy[8], gm[8];
+    h8_to_f(xr[v], x);
+    h8_to_f(dr[v], dy);
+    load_f8(g.gamma + 8 * v, gm);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float w = dy[e] * gm[e];
+      s1 += w;
+      s2 = fmaf(w, (x[e] - mu) * r, s2);
+    }
+  }
+  const float invk = 1.f / static_cast<float>(g.K);
+  s1 = row_sum<T>(s1, red[0]) * invk;
+  s2 = row_sum<T>(s2, red[1]) * invk;
+  if (g.rms) s1 = 0.f;
+  for (int v = threadIdx.x; v < nv; v += T) {
+    float x[8], dy[8], gm[8], rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    h8_to_f(xr[v], x);
+    h8_to_f(dr[v], dy);
+    load_f8(g.gamma + 8 * v, gm);
+    if (g.dres) h8_to_f(reinterpret_cast<const uint4*>(g.dres + o)[v], rs);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float xh = (x[e] - mu) * r;
+      x[e] = fmaf(r, dy[e] * gm[e] - s1 - xh * s2, rs[e]);
+    }
+    reinterpret_cast<uint4*>(g.dX + o)[v] = f_to_h8(x);
+  }
+}
+
+}  // namespace qlin

@@ -70,16 +70,35 @@ __device__ __forceinline__ size_t w8_tile_offset(int n, int k0, int KB) {
   return (blk * 128 + r) * 128 + ((chunk ^ (r & 7)) << 4) + (k0 & 15);
 }
 
+// Where the packers read W[k][n]: one [K][N] matrix, or (gated layers) the
+// gate and up projections [K][N / 2] whose channels alternate: channel 2j is
+// gate channel j, channel 2j + 1 up channel j.
+struct WeightSource {
+  const uint16_t* W;
+  int N;
+  __device__ __forceinline__ uint16_t operator()(int k, int n) const {
+    return __ldg(W + static_cast<size_t>(k) * N + n);
+  }
+};
+struct GatedSource {
+  const uint16_t* gate;
+  const uint16_t* up;
+  int F;
+  __device__ __forceinline__ uint16_t operator()(int k, int n) const {
+    return __ldg(((n & 1) ? up : gate) + static_cast<size_t>(k) * F + (n >> 1));
+  }
+};
+
 // Symmetric per-output-channel quantization:
 //   c_n = wmax_n / qmax,  q = clamp(rne(w * (qmax / wmax_n)), -qmax, qmax)   (fp32)
-template <int QMAX, bool W4>
-__global__ void pack_per_channel_kernel(const uint16_t* __restrict__ W, int K, int N,
-                                        uint8_t* __restrict__ codes, float* __restrict__ cscale) {
+template <int QMAX, bool W4, typename Src>
+__global__ void pack_per_channel_kernel(const Src W, int K, int N, uint8_t* __restrict__ codes,
+                                        float* __restrict__ cscale) {
   const int n = blockIdx.x * blockDim.x + threadIdx.x;
   if (n >= N) return;
   float wmax = 0.f;
   for (int k = 0; k < K; ++k) {
-    const float v = fabsf(h2f(W[static_cast<size_t>(k) * N + n]));
+    const float v = fabsf(h2f(W(k, n)));
     wmax = v > wmax ? v : wmax;
   }
   const float fq = static_cast<float>(QMAX);
@@ -88,7 +107,7 @@ __global__ void pack_per_channel_kernel(const uint16_t* __restrict__ W, int K, i
   for (int k0 = 0; k0 < K; k0 += 8) {
     int q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = rne_clamp(__fmul_rn(h2f(W[static_cast<size_t>(k0 + j) * N + n]), inv), QMAX);
+    for (int j = 0; j < 8; ++j) q[j] = rne_clamp(__fmul_rn(h2f(W(k0 + j, n)), inv), QMAX);
     const int KB = (K + 127) >> 7;
     if (W4) {
       *reinterpret_cast<uint32_t*>(codes + w4_tile_offset(n, k0, KB)) = pack8_nibbles(q);
@@ -101,9 +120,8 @@ __global__ void pack_per_channel_kernel(const uint16_t* __restrict__ W, int K, i
 // Per-group (128 input channels) INT4 with the folded requantization ratio:
 //   g = fp16(gmax / 7);  q4 = clamp(rne(w / g), -7, 7)
 //   c_n = 7 * max_j g / 127;  r = fp16(g / c_n)
-template <int GROUP>
-__global__ void pack_group_kernel(const uint16_t* __restrict__ W, int K, int N,
-                                  uint8_t* __restrict__ codes, float* __restrict__ cscale,
+template <int GROUP, typename Src>
+__global__ void pack_group_kernel(const Src W, int K, int N, uint8_t* __restrict__ codes, float* __restrict__ cscale,
                                   uint16_t* __restrict__ gscale, uint16_t* __restrict__ rfold) {
   const int n = blockIdx.x * blockDim.x + threadIdx.x;
   if (n >= N) return;
@@ -112,7 +130,7 @@ __global__ void pack_group_kernel(const uint16_t* __restrict__ W, int K, int N,
   for (int j = 0; j < G; ++j) {
     float gmax = 0.f;
     for (int k = j * GROUP; k < (j + 1) * GROUP; ++k) {
-      const float v = fabsf(h2f(W[static_cast<size_t>(k) * N + n]));
+      const float v = fabsf(h2f(W(k, n)));
       gmax = v > gmax ? v : gmax;
     }
     const uint16_t gh = f2h_bits(__fdiv_rn(gmax, 7.f));
@@ -129,7 +147,7 @@ __global__ void pack_group_kernel(const uint16_t* __restrict__ W, int K, int N,
       int q[8];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        const float w = h2f(W[static_cast<size_t>(k0 + t) * N + n]);
+        const float w = h2f(W(k0 + t, n));
         q[t] = ghf > 0.f ? rne_clamp(__fdiv_rn(w, ghf), 7) : 0;
       }
       *reinterpret_cast<uint32_t*>(codes + w4_tile_offset(n, k0, K >> 7)) = pack8_nibbles(q);
@@ -150,14 +168,15 @@ __device__ __forceinline__ size_t wot_tile_index(int n, int i, int IB) {
   return ((blk * 128 + r) * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15)) >> 1;
 }
 
-__global__ void pack_outliers_kernel(const uint16_t* __restrict__ W, int N, const int32_t* __restrict__ O,
+template <typename Src>
+__global__ void pack_outliers_kernel(const Src W, int N, const int32_t* __restrict__ O,
                                      int nO, uint16_t* __restrict__ W_Ot, float* __restrict__ wmaxO) {
   const int i = blockIdx.x;
   const int IB = (nO + 63) >> 6;
-  const uint16_t* row = W + static_cast<size_t>(O[i]) * N;
+  const int k = O[i];
   float m = 0.f;
   for (int n = threadIdx.x; n < N; n += blockDim.x) {
-    const uint16_t v = row[n];
+    const uint16_t v = W(k, n);
     const float f = fabsf(h2f(v));
     m = f > m ? f : m;
     W_Ot[wot_tile_index(n, i, IB)] = v;

@@ -17,7 +17,9 @@
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
 #include "backward.cuh"
+#include "dact.cuh"
 #include "gptq.cuh"
+#include "norm.cuh"
 #include "offq.cuh"
 #include "pack.cuh"
 #include "smooth.cuh"
@@ -244,7 +246,7 @@ struct GemmPlan {
 };
 
 bool use_pair(const GemmPlan& p, const qlin_weights* w);
-template <int FMT>
+template <int FMT, int EPI = kEpiPlain>
 int pair_max_clusters();
 
 // Work split of a launch on CTA pairs over `tiles` tiles of T steps (the
@@ -254,12 +256,12 @@ int pair_max_clusters();
 // steps into one contiguous range per pair (stream-K), so every pair ends
 // at about the same time.  With eight or more full waves the empty part of
 // the last one is small and tiles stay whole.
-void pair_split(GemmPlan& p, long long tiles, int T, int kb, int maxc) {
+void pair_split(GemmPlan& p, long long tiles, int T, int kb, int maxc, bool may_split) {
   if (maxc > kMaxPairs) maxc = kMaxPairs;
   p.pair_sk_tiles = 0;
   for (int c = 0; c <= kMaxPairs; ++c) p.pair_bnd[c] = 0u;
   const long long full = tiles / maxc, rem = tiles % maxc;
-  if (knob(QLIN_KNOB_PAIR_SPLIT) == 0 || rem == 0 || full >= 8 || maxc < 2) {
+  if (!may_split || knob(QLIN_KNOB_PAIR_SPLIT) == 0 || rem == 0 || full >= 8 || maxc < 2) {
     p.pair_ncl = static_cast<int>(tiles < maxc ? tiles : maxc);
     p.pair_dp = static_cast<int>(tiles);
     return;
@@ -286,7 +288,9 @@ void pair_split(GemmPlan& p, long long tiles, int T, int kb, int maxc) {
 // and run the INT8 kernel (QLIN_KNOB_WIDEN_MIN_M; 0 turns it off).
 int widen_min_m() { return static_cast<int>(knob(QLIN_KNOB_WIDEN_MIN_M)); }
 
-GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n) {
+// `fused` launches (a fused epilogue, one problem) keep whole tiles on CTA
+// pairs and widen INT4 ahead of them.
+GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused = false) {
   GemmPlan p{};
   p.nprob = n;
   p.bt = pick_bt(M);
@@ -362,12 +366,12 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n) {
   p.pacc_off = p.pcomp_off = p.pcnt_off = off;
   if (n == 1 && use_pair(p, ws[0])) {
     const GemmProb& q = p.pr[0];
-    const bool conv = p.widen && M <= convert_max_m();
+    const bool conv = p.widen && M <= convert_max_m() && !fused;
     const int maxc = !conv ? pair_max_clusters<kFmtW8>()
                            : (ws[0]->fmt == QLIN_W4_PERCHANNEL ? pair_max_clusters<kFmtW4PC>()
                                                                 : pair_max_clusters<kFmtW4G128>());
     const long long tiles = static_cast<long long>((q.tiles_n + 1) / 2) * q.tiles_m;
-    pair_split(p, tiles, q.kb + 2 * q.ncs, q.kb, maxc > 0 ? maxc : 1);
+    pair_split(p, tiles, q.kb + 2 * q.ncs, q.kb, maxc > 0 ? maxc : 1, !fused);
     if (p.pair_sk_tiles > 0) {
       const size_t part = size_t(2) * 256 * 128 * 4;  // one slot: both CTAs' 128 channels x 256 tokens
       off = round_up(off + size_t(2) * p.pair_ncl * part, kAlign);
@@ -381,15 +385,15 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n) {
   return p;
 }
 
-GemmPlan plan_gemm(int M, const qlin_weights* w) { return plan_gemm_group(M, &w, 1); }
+GemmPlan plan_gemm(int M, const qlin_weights* w, bool fused = false) { return plan_gemm_group(M, &w, 1, fused); }
 
 constexpr int kGroupMaxM = 64;  // token counts a grouped launch takes (decode-sized tiles)
 
 // ---------------------------------------------------------------- GEMM launch
-template <int FMT, int BT, int MAXP>
+template <int FMT, int BT, int MAXP, int EPI>
 qlin_status launch_gemm_t(GemmParams<MAXP>& prm, cudaStream_t stream) {
   using C = GemmCfg<FMT, BT>;
-  auto kern = gemm_kernel<FMT, BT, MAXP>;
+  auto kern = gemm_kernel<FMT, BT, MAXP, EPI>;
   static std::once_flag attr_once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(attr_once, [&] {
@@ -467,29 +471,37 @@ qlin_status launch_gemm_t(GemmParams<MAXP>& prm, cudaStream_t stream) {
 }
 
 // Grouped launches (MAXP > 1) take decode-sized token tiles only (<= 64).
-template <int FMT, int MAXP>
+template <int FMT, int MAXP, int EPI = kEpiPlain>
 qlin_status launch_gemm_fmt(int bt, GemmParams<MAXP>& prm, cudaStream_t stream) {
   switch (bt) {
-    case 16: return launch_gemm_t<FMT, 16, MAXP>(prm, stream);
-    case 32: return launch_gemm_t<FMT, 32, MAXP>(prm, stream);
-    case 64: return launch_gemm_t<FMT, 64, MAXP>(prm, stream);
+    case 16: return launch_gemm_t<FMT, 16, MAXP, EPI>(prm, stream);
+    case 32: return launch_gemm_t<FMT, 32, MAXP, EPI>(prm, stream);
+    case 64: return launch_gemm_t<FMT, 64, MAXP, EPI>(prm, stream);
     default:
       if constexpr (MAXP == 1) {
-        if (bt == 128) return launch_gemm_t<FMT, 128, 1>(prm, stream);
-        return launch_gemm_t<FMT, 256, 1>(prm, stream);
+        if (bt == 128) return launch_gemm_t<FMT, 128, 1, EPI>(prm, stream);
+        return launch_gemm_t<FMT, 256, 1, EPI>(prm, stream);
       } else {
         return fail(QLIN_ERR_SHAPE, "grouped GEMMs take at most %d tokens", kGroupMaxM);
       }
   }
 }
 
-// ---------------------------------------------------------------- CTA-pair GEMM (many tokens)
+// The same with the epilogue variant chosen at run time (one problem).
 template <int FMT>
+qlin_status launch_gemm_epi(int epi, int bt, GemmParams<1>& prm, cudaStream_t stream) {
+  if (epi == kEpiGated) return launch_gemm_fmt<FMT, 1, kEpiGated>(bt, prm, stream);
+  if (epi == kEpiAct) return launch_gemm_fmt<FMT, 1, kEpiAct>(bt, prm, stream);
+  return launch_gemm_fmt<FMT, 1>(bt, prm, stream);
+}
+
+// ---------------------------------------------------------------- CTA-pair GEMM (many tokens)
+template <int FMT, int EPI>
 int pair_max_clusters() {
   static int n = -1;
   static std::once_flag once;
   std::call_once(once, [] {
-    if (cudaFuncSetAttribute(gemm_pair_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(gemm_pair_kernel<FMT, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              PairCfg<FMT>::kSmem) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
@@ -507,7 +519,7 @@ int pair_max_clusters() {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int c = 0;
-    if (cudaOccupancyMaxActiveClusters(&c, gemm_pair_kernel<FMT>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&c, gemm_pair_kernel<FMT, EPI>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       c = 0;
     }
@@ -533,9 +545,10 @@ bool use_pair(const GemmPlan& p, const qlin_weights* w) {
 // FMT = kFmtW8: INT8 weight rows by TMA from `codes8` (the INT8 format, or
 // INT4 widened ahead); kFmtW4PC / kFmtW4G128: the layer's packed INT4 codes,
 // converted inside the kernel.
-template <int FMT>
+template <int FMT, int EPI = kEpiPlain>
 qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
-                             int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream) {
+                             int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream,
+                             const EpiArgs* epi = nullptr) {
   PairParams prm;
   memset(&prm, 0, sizeof(prm));
   PairArgs& g = prm.g;
@@ -559,7 +572,7 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
   g.tiles_m = q.tiles_m;
   g.tiles = g.tiles_n2 * g.tiles_m;
   const double x_bytes = static_cast<double>(M) * w->K;
-  const int maxc = pair_max_clusters<FMT>();
+  const int maxc = pair_max_clusters<FMT, EPI>();
   if (maxc < 1) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel: no 2-CTA cluster fits");
   int gm = static_cast<int>(std::lround(std::sqrt(static_cast<double>(maxc) * 256.0 / 256.0)));
   if (x_bytes <= 48.0 * 1024 * 1024) gm = g.tiles_m;
@@ -587,22 +600,43 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
                   static_cast<uint64_t>(q.tiles_n) * q.ncs * 128, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != QLIN_OK) return st;
   }
-  st = make_map(&prm.tmY, Y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N, M, 128, 256, CU_TENSOR_MAP_SWIZZLE_NONE);
+  constexpr int kYDiv = EPI == kEpiGated ? 2 : 1;  // gated: one output channel per pair
+  st = make_map(&prm.tmY, Y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N / kYDiv, M, 128 / kYDiv, 256,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
   if (st != QLIN_OK) return st;
-  cudaError_t e = launch_kc(gemm_pair_kernel<FMT>, dim3(static_cast<unsigned>(2 * g.ncl)),
+  if (EPI != kEpiPlain) {
+    g.epi = *epi;
+    if (epi->Z) {
+      st = make_map(&prm.tmZ, epi->Z, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N, M, 128, 256, CU_TENSOR_MAP_SWIZZLE_NONE);
+      if (st != QLIN_OK) return st;
+    }
+  }
+  cudaError_t e = launch_kc(gemm_pair_kernel<FMT, EPI>, dim3(static_cast<unsigned>(2 * g.ncl)),
                             dim3(PairCfg<FMT>::kThreads), PairCfg<FMT>::kSmem, stream, 2, prm);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
 }
 
+// INT8 operands on CTA pairs, with the epilogue variant chosen at run time.
+qlin_status launch_pair_w8(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
+                           int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream,
+                           const EpiArgs* epi, int variant) {
+  if (variant == kEpiGated)
+    return launch_gemm_pair<kFmtW8, kEpiGated>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+  if (variant == kEpiAct)
+    return launch_gemm_pair<kFmtW8, kEpiAct>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+  return launch_gemm_pair<kFmtW8>(p, w, Xq, a, Y, acc_debug, gws, codes8, cmul, stream);
+}
+
 // One GEMM launch over the problems of a plan.  Per problem q: weights
 // ws[q], the INT8 activations Xq[q], token scales a[q], output Y[q] and
 // (optional) acc_debug[q]; `gws` is the scratch laid out by the plan (each
-// problem's U, then the shared split-K slots and counters).
+// problem's U, then the shared split-K slots and counters).  `epi` and
+// `variant`: a fused epilogue (one problem, no acc_debug).
 template <int MAXP>
 qlin_status launch_gemm_group(const GemmPlan& p, const qlin_weights* const* ws, const int8_t* const* Xq,
                               const float* const* a, uint16_t* const* Y, int32_t* const* acc_debug, char* gws,
-                              cudaStream_t stream) {
+                              cudaStream_t stream, const EpiArgs* epi = nullptr, int variant = kEpiPlain) {
   qlin_status st = get_encoder();
   if (st != QLIN_OK) return st;
   static_assert(sizeof(GemmParams<MAXP>) <= 32000, "kernel parameter space");
@@ -644,9 +678,10 @@ qlin_status launch_gemm_group(const GemmPlan& p, const qlin_weights* const* ws, 
   args.cs = 1;
   args.ncl = 0;
   args.wdep = p.widen ? 1 : 0;
+  if (epi) args.epi = *epi;
   gemm_boundaries(prm.pr, p.nprob, p.grid, p.split, args.bnd);
   const int fmt = ws[0]->fmt;
-  if (p.widen && MAXP == 1 && use_pair(p, ws[0]) && p.pr[0].M <= convert_max_m()) {
+  if (p.widen && MAXP == 1 && !epi && use_pair(p, ws[0]) && p.pr[0].M <= convert_max_m()) {
     // INT4 on CTA pairs, converted inside the kernel (no widening pass)
     const qlin_weights* w = ws[0];
     const float cm = fmt == QLIN_W4_PERCHANNEL ? 0.0625f : 1.f;
@@ -671,13 +706,23 @@ qlin_status launch_gemm_group(const GemmPlan& p, const qlin_weights* const* ws, 
     prm.pr[0].codes = w8;
     prm.pr[0].cmul = fmt == QLIN_W4_PERCHANNEL ? 0.0625f : 1.f;
     if (MAXP == 1 && use_pair(p, w))
-      return launch_gemm_pair<kFmtW8>(p, w, Xq[0], a[0], Y[0], acc_debug ? acc_debug[0] : nullptr, gws, w8,
-                                      prm.pr[0].cmul, stream);
-    return launch_gemm_fmt<kFmtW8, MAXP>(p.bt, prm, stream);
+      return launch_pair_w8(p, w, Xq[0], a[0], Y[0], acc_debug ? acc_debug[0] : nullptr, gws, w8, prm.pr[0].cmul, stream,
+                            epi, variant);
+    if constexpr (MAXP == 1) return launch_gemm_epi<kFmtW8>(variant, p.bt, prm, stream);
+    else return launch_gemm_fmt<kFmtW8, MAXP>(p.bt, prm, stream);
   }
   if (MAXP == 1 && fmt == QLIN_W8_PERCHANNEL && use_pair(p, ws[0]))
-    return launch_gemm_pair<kFmtW8>(p, ws[0], Xq[0], a[0], Y[0], acc_debug ? acc_debug[0] : nullptr, gws,
-                            static_cast<const uint8_t*>(ws[0]->codes), 1.f, stream);
+    return launch_pair_w8(p, ws[0], Xq[0], a[0], Y[0], acc_debug ? acc_debug[0] : nullptr, gws,
+                          static_cast<const uint8_t*>(ws[0]->codes), 1.f, stream, epi, variant);
+  if constexpr (MAXP == 1) {
+    if (epi) {
+      switch (fmt) {
+        case QLIN_W4_PERCHANNEL: return launch_gemm_epi<kFmtW4PC>(variant, p.bt, prm, stream);
+        case QLIN_W4_G128: return launch_gemm_epi<kFmtW4G128>(variant, p.bt, prm, stream);
+        default: return launch_gemm_epi<kFmtW8>(variant, p.bt, prm, stream);
+      }
+    }
+  }
   switch (fmt) {
     case QLIN_W4_PERCHANNEL: return launch_gemm_fmt<kFmtW4PC, MAXP>(p.bt, prm, stream);
     case QLIN_W4_G128: return launch_gemm_fmt<kFmtW4G128, MAXP>(p.bt, prm, stream);
@@ -690,6 +735,12 @@ qlin_status launch_gemm(const qlin_weights* w, const int8_t* Xq, const float* a,
                         int32_t* acc_debug, char* gws, cudaStream_t stream) {
   const GemmPlan p = plan_gemm(M, w);
   return launch_gemm_group<1>(p, &w, &Xq, &a, &Y, acc_debug ? &acc_debug : nullptr, gws, stream);
+}
+
+// Single-problem GEMM launch with a fused epilogue.
+qlin_status launch_gemm_fused(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
+                              char* gws, cudaStream_t stream, const EpiArgs& epi, int variant) {
+  return launch_gemm_group<1>(p, &w, &Xq, &a, &Y, nullptr, gws, stream, &epi, variant);
 }
 
 // ---------------------------------------------------------------- act quant
@@ -805,20 +856,22 @@ qlin_status launch_quant(const uint16_t* X, int M, const qlin_weights* w, float*
   return launch_quant_group<1>(&w, &io, 1, M, gamma, update, stream);
 }
 
-size_t gemm_ws_bytes(int M, const qlin_weights* w) { return M > 0 ? plan_gemm(M, w).total : 0; }
+size_t gemm_ws_bytes(int M, const qlin_weights* w, bool fused = false) {
+  return M > 0 ? plan_gemm(M, w, fused).total : 0;
+}
 
 struct FwdLayout {
   size_t act, xq, a, xqo, gemm, total;
 };
 
-FwdLayout forward_layout(int M, const qlin_weights* w) {
+FwdLayout forward_layout(int M, const qlin_weights* w, bool fused = false) {
   FwdLayout L{};
   size_t off = 0;
   L.act = off; off = round_up(off + act_ws_bytes(w), kAlign);
   L.xq = off; off = round_up(off + size_t(M) * w->K, kAlign);
   L.a = off; off = round_up(off + size_t(M) * 4, kAlign);
   L.xqo = off; off = round_up(off + size_t(M) * w->n_outlier, kAlign);
-  L.gemm = off; off = round_up(off + gemm_ws_bytes(M, w), kAlign);
+  L.gemm = off; off = round_up(off + gemm_ws_bytes(M, w, fused), kAlign);
   L.total = off;
   return L;
 }
@@ -938,10 +991,10 @@ BwdPlan plan_backward(int M, const qlin_weights* w, bool split) {
   return p;
 }
 
-template <int FMT>
+template <int FMT, bool PRE>
 qlin_status launch_backward_t(const CUtensorMap& tm, const BwdArgs& args, cudaStream_t stream) {
   using C = BwdCfg<FMT>;
-  auto kern = backward_dx_kernel<FMT>;
+  auto kern = backward_dx_kernel<FMT, PRE>;
   static std::once_flag attr_once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(attr_once, [&] {
@@ -952,6 +1005,238 @@ qlin_status launch_backward_t(const CUtensorMap& tm, const BwdArgs& args, cudaSt
   cudaError_t e = launch_k(kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, tm, args);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "backward_dx_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
+}
+
+// The input gradient's launch.  PRE: dY holds the scaled gradients of
+// dact.cuh and `rowscale` the factors that undo their rows' scales.
+template <bool PRE>
+qlin_status launch_backward(const qlin_weights* w, const uint16_t* dY, int M, const float* s, uint16_t* dX,
+                            const float* rowscale, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  qlin_status st = get_encoder();
+  if (st != QLIN_OK) return st;
+  CUtensorMap tm;
+  st = make_map(&tm, dY, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->N, M, 64, 256, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != QLIN_OK) return st;
+  const int nO = w->n_outlier;
+  BwdArgs args;
+  args.codes = static_cast<const uint8_t*>(w->codes);
+  args.rfold = w->fold_ratio;
+  args.wot = w->W_Ot;
+  args.cscale = w->chan_scale;
+  args.oidx = w->outlier_idx;
+  args.s = s;
+  args.dX = dX;
+  args.M = M;
+  args.N = w->N;
+  args.K = w->K;
+  args.nO = nO;
+  args.rowscale = rowscale;
+  args.kbs = (w->K + 127) / 128;
+  args.nib = (nO + 63) / 64;
+  args.nsteps = (w->N + 63) / 64;
+  // the split plan needs the whole workspace it asks for; with none (or a
+  // smaller one) every tile runs whole
+  BwdPlan p = plan_backward(M, w, true);
+  if (p.bytes && (!workspace || ws_bytes < p.bytes)) p = plan_backward(M, w, false);
+  args.ntk = p.ntk;
+  args.full = p.full;
+  args.tsplit = p.tsplit;
+  args.part = p.bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_off) : nullptr;
+  args.cnt = p.bytes ? reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + p.cnt_off) : nullptr;
+  switch (w->fmt) {
+    case QLIN_W4_PERCHANNEL: return launch_backward_t<kFmtW4PC, PRE>(tm, args, stream);
+    case QLIN_W4_G128: return launch_backward_t<kFmtW4G128, PRE>(tm, args, stream);
+    default: return launch_backward_t<kFmtW8, PRE>(tm, args, stream);
+  }
+}
+
+// ---------------------------------------------------------------- packing
+// Quantize and pack from one weight source (checked by the caller).
+template <typename Src>
+qlin_status pack_from(const Src src, const int32_t* O_host, const qlin_weights* w, cudaStream_t stream) {
+  const int K = w->K, N = w->N, nO = w->n_outlier;
+  if (nO > 0) {
+    if (!O_host) return fail(QLIN_ERR_ARG, "O_host is NULL with n_outlier=%d", nO);
+    for (int i = 0; i < nO; ++i) {
+      if (O_host[i] < 0 || O_host[i] >= K) return fail(QLIN_ERR_ARG, "O[%d]=%d outside [0, K)", i, O_host[i]);
+      if (i > 0 && O_host[i] <= O_host[i - 1]) return fail(QLIN_ERR_ARG, "O is not strictly increasing at %d", i);
+    }
+  }
+  const int threads = 128;
+  const int blocks = (N + threads - 1) / threads;
+  uint8_t* codes = static_cast<uint8_t*>(w->codes);
+  const Layout L = weights_layout(K, N, w->fmt, nO);
+  QLIN_CUDA_TRY(cudaMemsetAsync(codes, 0, L.chan - L.codes, stream));  // tile padding is zero
+  switch (w->fmt) {
+    case QLIN_W4_PERCHANNEL:
+      pack_per_channel_kernel<7, true, Src><<<blocks, threads, 0, stream>>>(src, K, N, codes, w->chan_scale);
+      break;
+    case QLIN_W8_PERCHANNEL:
+      pack_per_channel_kernel<127, false, Src><<<blocks, threads, 0, stream>>>(src, K, N, codes, w->chan_scale);
+      break;
+    default:
+      pack_group_kernel<128, Src><<<blocks, threads, 0, stream>>>(src, K, N, codes, w->chan_scale, w->group_scale,
+                                                             w->fold_ratio);
+  }
+  QLIN_LAUNCH_CHECK("pack kernel");
+  if (nO > 0) {
+    QLIN_CUDA_TRY(cudaMemcpyAsync(w->outlier_idx, O_host, size_t(nO) * 4, cudaMemcpyHostToDevice, stream));
+    QLIN_CUDA_TRY(cudaMemsetAsync(w->W_Ot, 0, L.wmax - L.wot, stream));
+    pack_outliers_kernel<Src><<<nO, 256, 0, stream>>>(src, N, w->outlier_idx, nO, w->W_Ot, w->wmax_O);
+    QLIN_LAUNCH_CHECK("pack_outliers_kernel");
+  }
+  return QLIN_OK;
+}
+
+// ---------------------------------------------------------------- fused layers and norms
+qlin_status check_act(int32_t act) {
+  if (act < QLIN_ACT_NONE || act > QLIN_ACT_SILU) return fail(QLIN_ERR_ARG, "unknown activation %d", act);
+  return QLIN_OK;
+}
+
+qlin_status forward_fused(const uint16_t* X, int32_t M, const qlin_weights* w, float* s, float gamma, int32_t update,
+                          const EpiArgs& epi, int variant, uint16_t* Y, void* workspace, size_t ws_bytes,
+                          cudaStream_t stream) {
+  qlin_status st = check_weights(w);
+  if (st != QLIN_OK) return st;
+  st = check_act(epi.act);
+  if (st != QLIN_OK) return st;
+  if (M < 0) return fail(QLIN_ERR_ARG, "M=%d is negative", M);
+  if (!(gamma >= 0.f && gamma <= 1.f)) return fail(QLIN_ERR_ARG, "gamma=%g outside [0, 1]", double(gamma));
+  if (M == 0) return QLIN_OK;
+  const int nO = w->n_outlier;
+  if (!X || !Y) return fail(QLIN_ERR_ARG, "X/Y is NULL");
+  if (nO > 0 && !s) return fail(QLIN_ERR_ARG, "s is NULL with n_outlier=%d", nO);
+  if (epi.Z && epi.Z == Y) return fail(QLIN_ERR_ARG, "Z and Y are the same buffer");
+  if (epi.Z && epi.Z == epi.residual) return fail(QLIN_ERR_ARG, "Z and residual are the same buffer");
+  if (!aligned16(X) || !aligned16(Y) || (s && !aligned16(s)) || (epi.bias && !aligned16(epi.bias)) ||
+      (epi.residual && !aligned16(epi.residual)) || (epi.Z && !aligned16(epi.Z)))
+    return fail(QLIN_ERR_ALIGN, "X/Y/s/bias/residual/Z is not 16-byte aligned");
+  const FwdLayout L = forward_layout(M, w, true);
+  if (ws_bytes < L.total || !workspace) return fail(QLIN_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, L.total);
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return fail(QLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
+  char* ws = static_cast<char*>(workspace);
+  int8_t* Xq = reinterpret_cast<int8_t*>(ws + L.xq);
+  float* a = reinterpret_cast<float*>(ws + L.a);
+  int8_t* XqO = nO > 0 ? reinterpret_cast<int8_t*>(ws + L.xqo) : nullptr;
+  char* gws = ws + L.gemm;
+  const GemmPlan p = plan_gemm(M, w, true);
+  uint16_t* U = nO > 0 ? reinterpret_cast<uint16_t*>(gws + p.u_off[0]) : nullptr;
+  st = launch_quant(X, M, w, s, gamma, update, Xq, a, XqO, U, ws + L.act, stream);
+  if (st != QLIN_OK) return st;
+  return launch_gemm_fused(p, w, Xq, a, Y, gws, stream, epi, variant);
+}
+
+// Row groups of a column-sum launch over M rows of `nv` 8-element vectors
+// (128 per CTA): about four CTAs per SM, at least eight rows each.
+int column_groups(int M, int nv) {
+  const int gx = (nv + 127) / 128;
+  const int want = (4 * sm_count() + gx - 1) / gx;
+  const int most = (M + 7) / 8;
+  const int G = want < most ? want : most;
+  return G < 1 ? 1 : (G > 65535 ? 65535 : G);
+}
+
+// Partial column sums [G][K] (twice that, dgamma then dbeta, for a norm) to
+// their totals.
+qlin_status launch_column_sum(const float* part, int G, int K, float* out0, float* out1, cudaStream_t stream) {
+  cudaError_t e = launch_k(column_sum_kernel, dim3((K + 31) / 32, out1 ? 2 : 1), dim3(256), 0, stream, part, G, K, out0,
+                           out1);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "column_sum_kernel launch failed: %s", cudaGetErrorString(e));
+  return QLIN_OK;
+}
+
+// Workspace of a fused layer's backward pass: the scaled dZ, the rows'
+// factors, the bias gradient's partial sums, the input gradient's split
+// tiles (zero before the first use, left zero).
+struct FusedBwdLayout {
+  size_t split, dz, rows, part, total;
+  int G;
+};
+FusedBwdLayout fused_bwd_layout(int M, const qlin_weights* w) {
+  FusedBwdLayout L{};
+  size_t off = 0;
+  L.split = off; off = round_up(off + plan_backward(M, w, true).bytes, kAlign);
+  L.dz = off; off = round_up(off + size_t(M) * w->N * 2, kAlign);
+  L.rows = off; off = round_up(off + size_t(M) * 4, kAlign);
+  L.G = column_groups(M, w->N / 8);
+  L.part = off; off = round_up(off + size_t(L.G) * w->N * 4, kAlign);
+  L.total = off;
+  return L;
+}
+
+template <bool GATED>
+qlin_status backward_fused(const qlin_weights* w, const uint16_t* dY, const uint16_t* Z, int32_t act, int32_t M,
+                           const float* s, uint16_t* dX, float* dbias, void* workspace, size_t ws_bytes,
+                           cudaStream_t stream) {
+  qlin_status st = check_weights(w);
+  if (st != QLIN_OK) return st;
+  st = check_act(act);
+  if (st != QLIN_OK) return st;
+  if (M < 0) return fail(QLIN_ERR_ARG, "M=%d is negative", M);
+  if (M > 65535 * 128) return fail(QLIN_ERR_SHAPE, "M=%d exceeds %d", M, 65535 * 128);
+  if (dbias && !aligned16(dbias)) return fail(QLIN_ERR_ALIGN, "dbias is not 16-byte aligned");
+  if (M == 0) {  // no rows: the bias's gradient is a sum over nothing
+    if (dbias) QLIN_CUDA_TRY(cudaMemsetAsync(dbias, 0, size_t(w->N) * 4, stream));
+    return QLIN_OK;
+  }
+  const int nO = w->n_outlier;
+  const bool needs_z = GATED || act != QLIN_ACT_NONE;
+  if (!dX && !dbias) return fail(QLIN_ERR_ARG, "dX and dbias are both NULL");
+  if (!dY || (needs_z && !Z)) return fail(QLIN_ERR_ARG, "dY/Z is NULL");
+  if (nO > 0 && dX && !s) return fail(QLIN_ERR_ARG, "s is NULL with n_outlier=%d", nO);
+  if (!aligned16(dY) || (Z && !aligned16(Z)) || (dX && !aligned16(dX)) || (s && !aligned16(s)))
+    return fail(QLIN_ERR_ALIGN, "dY/Z/dX/s is not 16-byte aligned");
+  const FusedBwdLayout L = fused_bwd_layout(M, w);
+  if (ws_bytes < L.total || !workspace) return fail(QLIN_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, L.total);
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return fail(QLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
+  char* ws = static_cast<char*>(workspace);
+  DactArgs g{};
+  g.dY = dY;
+  g.Z = Z;
+  g.cscale = w->chan_scale;
+  g.dZ = reinterpret_cast<uint16_t*>(ws + L.dz);
+  g.rowscale = reinterpret_cast<float*>(ws + L.rows);
+  g.part = reinterpret_cast<float*>(ws + L.part);
+  g.cmul = w->fmt == QLIN_W4_PERCHANNEL ? 0.0625f : 1.f;
+  g.M = M;
+  g.N = w->N;
+  g.act = act;
+  g.G = L.G;
+  if (dbias) {
+    cudaError_t e = launch_k(dact_columns_kernel<GATED>, dim3((w->N / 8 + 127) / 128, L.G), dim3(128), 0, stream, g);
+    if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_columns_kernel launch failed: %s", cudaGetErrorString(e));
+    st = launch_column_sum(g.part, L.G, w->N, dbias, nullptr, stream);
+    if (st != QLIN_OK) return st;
+  }
+  if (!dX) return QLIN_OK;
+  cudaError_t e = launch_k(dact_rows_kernel<GATED>, dim3(static_cast<unsigned>(M)), dim3(kDactThreads), 0, stream, g);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_rows_kernel launch failed: %s", cudaGetErrorString(e));
+  return launch_backward<true>(w, g.dZ, M, s, dX, g.rowscale, ws + L.split, L.dz - L.split, stream);
+}
+
+qlin_status check_norm(int32_t M, int32_t K, int32_t kind) {
+  if (kind != QLIN_NORM_LAYER && kind != QLIN_NORM_RMS) return fail(QLIN_ERR_ARG, "unknown norm kind %d", kind);
+  if (M < 0 || K <= 0) return fail(QLIN_ERR_ARG, "bad sizes M=%d K=%d", M, K);
+  if (K % 32 != 0 || K > 65536) return fail(QLIN_ERR_SHAPE, "K=%d must be a multiple of 32, at most 65536", K);
+  return QLIN_OK;
+}
+
+template <int T, int VPT>
+cudaError_t launch_norm_t(const NormFwdArgs& g, cudaStream_t stream) {
+  const unsigned grid = T == 32 ? (static_cast<unsigned>(g.M) + 3) / 4 : static_cast<unsigned>(g.M);
+  return launch_k(norm_forward_kernel<T, VPT>, dim3(grid), dim3(T == 32 ? 128 : T), 0, stream, g);
+}
+
+struct NormBwdLayout {
+  int G;
+  size_t total;
+};
+NormBwdLayout norm_bwd_layout(int M, int K) {
+  NormBwdLayout L{};
+  L.G = column_groups(M, K / 8);
+  L.total = M > 0 ? round_up(size_t(2) * L.G * K * 4, kAlign) : 0;
+  return L;
 }
 
 }  // namespace
@@ -1012,44 +1297,21 @@ qlin_status qlin_weights_bind(qlin_weights* w, int32_t K, int32_t N, int32_t fmt
   return QLIN_OK;
 }
 
-qlin_status qlin_pack_weights(const uint16_t* W, const int32_t* O_host, const qlin_weights* w, void* stream_) {
+qlin_status qlin_pack_weights(const uint16_t* W, const int32_t* O_host, const qlin_weights* w, void* stream) {
   qlin_status st = check_weights(w);
   if (st != QLIN_OK) return st;
   if (!W) return fail(QLIN_ERR_ARG, "W is NULL");
   if (!aligned16(W)) return fail(QLIN_ERR_ALIGN, "W is not 16-byte aligned");
-  const int K = w->K, N = w->N, nO = w->n_outlier;
-  if (nO > 0) {
-    if (!O_host) return fail(QLIN_ERR_ARG, "O_host is NULL with n_outlier=%d", nO);
-    for (int i = 0; i < nO; ++i) {
-      if (O_host[i] < 0 || O_host[i] >= K) return fail(QLIN_ERR_ARG, "O[%d]=%d outside [0, K)", i, O_host[i]);
-      if (i > 0 && O_host[i] <= O_host[i - 1]) return fail(QLIN_ERR_ARG, "O is not strictly increasing at %d", i);
-    }
-  }
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const int threads = 128;
-  const int blocks = (N + threads - 1) / threads;
-  uint8_t* codes = static_cast<uint8_t*>(w->codes);
-  const Layout L = weights_layout(K, N, w->fmt, nO);
-  QLIN_CUDA_TRY(cudaMemsetAsync(codes, 0, L.chan - L.codes, stream));  // tile padding is zero
-  switch (w->fmt) {
-    case QLIN_W4_PERCHANNEL:
-      pack_per_channel_kernel<7, true><<<blocks, threads, 0, stream>>>(W, K, N, codes, w->chan_scale);
-      break;
-    case QLIN_W8_PERCHANNEL:
-      pack_per_channel_kernel<127, false><<<blocks, threads, 0, stream>>>(W, K, N, codes, w->chan_scale);
-      break;
-    default:
-      pack_group_kernel<128><<<blocks, threads, 0, stream>>>(W, K, N, codes, w->chan_scale, w->group_scale,
-                                                             w->fold_ratio);
-  }
-  QLIN_LAUNCH_CHECK("pack kernel");
-  if (nO > 0) {
-    QLIN_CUDA_TRY(cudaMemcpyAsync(w->outlier_idx, O_host, size_t(nO) * 4, cudaMemcpyHostToDevice, stream));
-    QLIN_CUDA_TRY(cudaMemsetAsync(w->W_Ot, 0, L.wmax - L.wot, stream));
-    pack_outliers_kernel<<<nO, 256, 0, stream>>>(W, N, w->outlier_idx, nO, w->W_Ot, w->wmax_O);
-    QLIN_LAUNCH_CHECK("pack_outliers_kernel");
-  }
-  return QLIN_OK;
+  return pack_from(WeightSource{W, w->N}, O_host, w, static_cast<cudaStream_t>(stream));
+}
+
+qlin_status qlin_pack_gated(const uint16_t* W_gate, const uint16_t* W_up, const int32_t* O_host, const qlin_weights* w,
+                            void* stream) {
+  qlin_status st = check_weights(w);
+  if (st != QLIN_OK) return st;
+  if (!W_gate || !W_up) return fail(QLIN_ERR_ARG, "W_gate/W_up is NULL");
+  if (!aligned16(W_gate) || !aligned16(W_up)) return fail(QLIN_ERR_ALIGN, "W_gate/W_up is not 16-byte aligned");
+  return pack_from(GatedSource{W_gate, W_up, w->N / 2}, O_host, w, static_cast<cudaStream_t>(stream));
 }
 
 qlin_status qlin_quant_act_workspace(int32_t M, const qlin_weights* w, size_t* bytes) {
@@ -1196,41 +1458,7 @@ qlin_status qlin_backward_dx(const qlin_weights* w, const uint16_t* dY, int32_t 
   if (nO > 0 && !s) return fail(QLIN_ERR_ARG, "s is NULL with n_outlier=%d", nO);
   if (!aligned16(dY) || !aligned16(dX) || (s && !aligned16(s)))
     return fail(QLIN_ERR_ALIGN, "a backward buffer is not 16-byte aligned");
-  st = get_encoder();
-  if (st != QLIN_OK) return st;
-  CUtensorMap tm;
-  st = make_map(&tm, dY, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->N, M, 64, 256, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st != QLIN_OK) return st;
-  BwdArgs args;
-  args.codes = static_cast<const uint8_t*>(w->codes);
-  args.rfold = w->fold_ratio;
-  args.wot = w->W_Ot;
-  args.cscale = w->chan_scale;
-  args.oidx = w->outlier_idx;
-  args.s = s;
-  args.dX = dX;
-  args.M = M;
-  args.N = w->N;
-  args.K = w->K;
-  args.nO = nO;
-  args.kbs = (w->K + 127) / 128;
-  args.nib = (nO + 63) / 64;
-  args.nsteps = (w->N + 63) / 64;
-  // the split plan needs the whole workspace it asks for; with none (or a
-  // smaller one) every tile runs whole
-  BwdPlan p = plan_backward(M, w, true);
-  if (p.bytes && (!workspace || ws_bytes < p.bytes)) p = plan_backward(M, w, false);
-  args.ntk = p.ntk;
-  args.full = p.full;
-  args.tsplit = p.tsplit;
-  args.part = p.bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_off) : nullptr;
-  args.cnt = p.bytes ? reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + p.cnt_off) : nullptr;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  switch (w->fmt) {
-    case QLIN_W4_PERCHANNEL: return launch_backward_t<kFmtW4PC>(tm, args, stream);
-    case QLIN_W4_G128: return launch_backward_t<kFmtW4G128>(tm, args, stream);
-    default: return launch_backward_t<kFmtW8>(tm, args, stream);
-  }
+  return launch_backward<false>(w, dY, M, s, dX, nullptr, workspace, ws_bytes, static_cast<cudaStream_t>(stream_));
 }
 
 qlin_status qlin_forward_workspace(int32_t M, const qlin_weights* w, size_t* bytes) {
@@ -1266,6 +1494,132 @@ qlin_status qlin_forward(const uint16_t* X, int32_t M, const qlin_weights* w, fl
   st = launch_quant(X, M, w, s, gamma, update_momentum, Xq, a, XqO, U, ws + L.act, stream);
   if (st != QLIN_OK) return st;
   return launch_gemm(w, Xq, a, M, Y, nullptr, gws, stream);
+}
+
+qlin_status qlin_forward_act_workspace(int32_t M, const qlin_weights* w, size_t* bytes) {
+  qlin_status st = check_weights(w);
+  if (st != QLIN_OK) return st;
+  if (!bytes || M < 0) return fail(QLIN_ERR_ARG, "bad arguments");
+  *bytes = forward_layout(M, w, true).total;
+  return QLIN_OK;
+}
+
+qlin_status qlin_forward_act(const uint16_t* X, int32_t M, const qlin_weights* w, float* s, float gamma,
+                             int32_t update_momentum, int32_t act, const float* bias, const uint16_t* residual,
+                             uint16_t* Z, uint16_t* Y, void* workspace, size_t ws_bytes, void* stream) {
+  const EpiArgs e{bias, residual, Z, act};
+  return forward_fused(X, M, w, s, gamma, update_momentum, e, kEpiAct, Y, workspace, ws_bytes,
+                       static_cast<cudaStream_t>(stream));
+}
+
+qlin_status qlin_forward_gated_workspace(int32_t M, const qlin_weights* w, size_t* bytes) {
+  return qlin_forward_act_workspace(M, w, bytes);
+}
+
+qlin_status qlin_forward_gated(const uint16_t* X, int32_t M, const qlin_weights* w, float* s, float gamma,
+                               int32_t update_momentum, int32_t act, const float* bias, uint16_t* Z, uint16_t* H,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  const EpiArgs e{bias, nullptr, Z, act};
+  return forward_fused(X, M, w, s, gamma, update_momentum, e, kEpiGated, H, workspace, ws_bytes,
+                       static_cast<cudaStream_t>(stream));
+}
+
+qlin_status qlin_backward_act_workspace(int32_t M, const qlin_weights* w, size_t* bytes) {
+  qlin_status st = check_weights(w);
+  if (st != QLIN_OK) return st;
+  if (!bytes || M < 0) return fail(QLIN_ERR_ARG, "bad arguments");
+  *bytes = M > 0 ? fused_bwd_layout(M, w).total : 0;
+  return QLIN_OK;
+}
+
+qlin_status qlin_backward_act(const qlin_weights* w, const uint16_t* dY, const uint16_t* Z, int32_t act, int32_t M,
+                              const float* s, uint16_t* dX, float* dbias, void* workspace, size_t ws_bytes,
+                              void* stream) {
+  return backward_fused<false>(w, dY, Z, act, M, s, dX, dbias, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+qlin_status qlin_backward_gated_workspace(int32_t M, const qlin_weights* w, size_t* bytes) {
+  return qlin_backward_act_workspace(M, w, bytes);
+}
+
+qlin_status qlin_backward_gated(const qlin_weights* w, const uint16_t* dH, const uint16_t* Z, int32_t act, int32_t M,
+                                const float* s, uint16_t* dX, float* dbias, void* workspace, size_t ws_bytes,
+                                void* stream) {
+  return backward_fused<true>(w, dH, Z, act, M, s, dX, dbias, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+qlin_status qlin_norm_forward(const uint16_t* X, int32_t M, int32_t K, int32_t kind, const float* gamma,
+                              const float* beta, float eps, uint16_t* Y, float* mean, float* rstd, void* stream_) {
+  qlin_status st = check_norm(M, K, kind);
+  if (st != QLIN_OK) return st;
+  if (!(eps > 0.f) || std::isinf(eps)) return fail(QLIN_ERR_ARG, "eps=%g must be positive and finite", double(eps));
+  if (M == 0) return QLIN_OK;
+  if (!X || !gamma || !Y) return fail(QLIN_ERR_ARG, "X/gamma/Y is NULL");
+  if (!aligned16(X) || !aligned16(gamma) || !aligned16(Y) || (beta && !aligned16(beta)) || (mean && !aligned16(mean)) ||
+      (rstd && !aligned16(rstd)))
+    return fail(QLIN_ERR_ALIGN, "a norm buffer is not 16-byte aligned");
+  const NormFwdArgs g{X, gamma, beta, Y, kind == QLIN_NORM_RMS ? nullptr : mean, rstd, M, K, kind == QLIN_NORM_RMS, eps};
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const int nv = K / 8;
+  cudaError_t e;
+  if (nv <= 32) e = launch_norm_t<32, 1>(g, stream);
+  else if (nv <= 128) e = launch_norm_t<32, 4>(g, stream);
+  else if (nv <= 512) e = launch_norm_t<128, 4>(g, stream);
+  else if (nv <= 1024) e = launch_norm_t<256, 4>(g, stream);
+  else if (nv <= 2048) e = launch_norm_t<512, 4>(g, stream);
+  else e = launch_norm_t<1024, 8>(g, stream);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "norm_forward_kernel launch failed: %s", cudaGetErrorString(e));
+  return QLIN_OK;
+}
+
+qlin_status qlin_norm_backward_workspace(int32_t M, int32_t K, size_t* bytes) {
+  qlin_status st = check_norm(M, K, QLIN_NORM_LAYER);
+  if (st != QLIN_OK) return st;
+  if (!bytes) return fail(QLIN_ERR_ARG, "bytes is NULL");
+  *bytes = norm_bwd_layout(M, K).total;
+  return QLIN_OK;
+}
+
+qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M, int32_t K, int32_t kind,
+                               const float* gamma, const float* mean, const float* rstd, const uint16_t* dres,
+                               uint16_t* dX, float* dgamma, float* dbeta, void* workspace, size_t ws_bytes,
+                               void* stream_) {
+  qlin_status st = check_norm(M, K, kind);
+  if (st != QLIN_OK) return st;
+  const bool rms = kind == QLIN_NORM_RMS;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if ((dgamma && !aligned16(dgamma)) || (dbeta && !aligned16(dbeta)))
+    return fail(QLIN_ERR_ALIGN, "dgamma/dbeta is not 16-byte aligned");
+  if (M == 0) {  // no rows: sums over nothing
+    if (dgamma) QLIN_CUDA_TRY(cudaMemsetAsync(dgamma, 0, size_t(K) * 4, stream));
+    if (dbeta) QLIN_CUDA_TRY(cudaMemsetAsync(dbeta, 0, size_t(K) * 4, stream));
+    return QLIN_OK;
+  }
+  if (!dX && !dgamma && !dbeta) return fail(QLIN_ERR_ARG, "dX, dgamma and dbeta are all NULL");
+  if (!dY || !X || !gamma || !rstd || (!rms && !mean)) return fail(QLIN_ERR_ARG, "dY/X/gamma/mean/rstd is NULL");
+  if (!aligned16(dY) || !aligned16(X) || !aligned16(gamma) || !aligned16(rstd) || (mean && !aligned16(mean)) ||
+      (dres && !aligned16(dres)) || (dX && !aligned16(dX)))
+    return fail(QLIN_ERR_ALIGN, "a norm buffer is not 16-byte aligned");
+  NormBwdArgs g{dY, X, gamma, rms ? nullptr : mean, rstd, dres, dX, nullptr, M, K, rms, 0};
+  if (dgamma || dbeta) {
+    const NormBwdLayout L = norm_bwd_layout(M, K);
+    if (ws_bytes < L.total || !workspace) return fail(QLIN_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, L.total);
+    if (reinterpret_cast<uintptr_t>(workspace) % kAlign)
+      return fail(QLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
+    g.part = static_cast<float*>(workspace);
+    g.G = L.G;
+    // before dX, which may replace dY or X
+    cudaError_t e = launch_k(norm_columns_kernel, dim3((K / 8 + 127) / 128, L.G), dim3(128), 0, stream, g);
+    if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "norm_columns_kernel launch failed: %s", cudaGetErrorString(e));
+    st = launch_column_sum(g.part, L.G, K, dgamma, dbeta, stream);
+    if (st != QLIN_OK) return st;
+  }
+  if (!dX) return QLIN_OK;
+  const dim3 grid(static_cast<unsigned>(M));
+  cudaError_t e = K <= 1024 ? launch_k(norm_rows_kernel<128>, grid, dim3(128), 0, stream, g)
+                            : launch_k(norm_rows_kernel<512>, grid, dim3(512), 0, stream, g);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "norm_rows_kernel launch failed: %s", cudaGetErrorString(e));
+  return QLIN_OK;
 }
 
 #ifdef QLIN_TRACE

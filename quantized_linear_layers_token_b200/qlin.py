@@ -21,6 +21,15 @@ QLIN_W4_PERCHANNEL = 0
 QLIN_W4_G128 = 1
 QLIN_W8_PERCHANNEL = 2
 
+QLIN_ACT_NONE = 0
+QLIN_ACT_RELU = 1
+QLIN_ACT_GELU = 2
+QLIN_ACT_GELU_TANH = 3
+QLIN_ACT_SILU = 4
+
+QLIN_NORM_LAYER = 0
+QLIN_NORM_RMS = 1
+
 STATUS = {0: "QLIN_OK", 1: "QLIN_ERR_ARG", 2: "QLIN_ERR_SHAPE", 3: "QLIN_ERR_ALIGN",
           4: "QLIN_ERR_WORKSPACE", 5: "QLIN_ERR_CUDA", 6: "QLIN_ERR_TIMEOUT"}
 
@@ -33,7 +42,10 @@ EXPORTED = [
     "qlin_forward_grouped", "qlin_gptq_workspace", "qlin_gptq_quantize", "qlin_smooth_search_workspace",
     "qlin_smooth_search", "qlin_offq_codes_bytes", "qlin_offq_rotate_weights", "qlin_offq_pack",
     "qlin_offq_quant_act", "qlin_offq_gemm_workspace", "qlin_offq_gemm", "qlin_offq_forward_workspace",
-    "qlin_offq_forward",
+    "qlin_offq_forward", "qlin_forward_act_workspace", "qlin_forward_act", "qlin_backward_act_workspace",
+    "qlin_backward_act", "qlin_pack_gated", "qlin_forward_gated_workspace", "qlin_forward_gated",
+    "qlin_backward_gated_workspace", "qlin_backward_gated", "qlin_norm_forward", "qlin_norm_backward_workspace",
+    "qlin_norm_backward",
 ]
 
 # test / measurement knobs (qlin_debug_set, include/qlin.h)
@@ -118,6 +130,18 @@ def lib() -> ctypes.CDLL:
             "qlin_offq_gemm": [P, P, P, I32, I32, I32, P, P, P, P, P, SZ, P],
             "qlin_offq_forward_workspace": [I32, I32, I32, ctypes.POINTER(SZ)],
             "qlin_offq_forward": [P, I32, I32, I32, P, P, P, P, P, P, SZ, P],
+            "qlin_forward_act_workspace": [I32, W, ctypes.POINTER(SZ)],
+            "qlin_forward_act": [P, I32, W, P, F32, I32, I32, P, P, P, P, P, SZ, P],
+            "qlin_backward_act_workspace": [I32, W, ctypes.POINTER(SZ)],
+            "qlin_backward_act": [W, P, P, I32, I32, P, P, P, P, SZ, P],
+            "qlin_pack_gated": [P, P, P, W, P],
+            "qlin_forward_gated_workspace": [I32, W, ctypes.POINTER(SZ)],
+            "qlin_forward_gated": [P, I32, W, P, F32, I32, I32, P, P, P, P, SZ, P],
+            "qlin_backward_gated_workspace": [I32, W, ctypes.POINTER(SZ)],
+            "qlin_backward_gated": [W, P, P, I32, I32, P, P, P, P, SZ, P],
+            "qlin_norm_forward": [P, I32, I32, I32, P, P, F32, P, P, P, P],
+            "qlin_norm_backward_workspace": [I32, I32, ctypes.POINTER(SZ)],
+            "qlin_norm_backward": [P, P, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P],
         }
         for name, argt in sigs.items():
             fn = getattr(L, name)
@@ -333,6 +357,120 @@ def qlin_backward_dx(w: qlin_weights, dY, M: int, s, dX, workspace=None, ws_byte
                                   _stream(stream)), "qlin_backward_dx")
 
 
+def _buf(t, dtype, n: int, name: str) -> int | None:
+    """Device address of an argument of the fused layers: None, an address, or
+    a dense tensor of at least n elements of `dtype` on the current device
+    (the stream's)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, {n} are needed")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
+
+
+def qlin_forward_act_workspace(M: int, w: qlin_weights) -> int:
+    return _size(lib().qlin_forward_act_workspace, M, ctypes.byref(w))
+
+
+def qlin_forward_act(X, M: int, w: qlin_weights, s, gamma: float, update_momentum: bool, Y, workspace, ws_bytes: int,
+                     act: int = QLIN_ACT_NONE, bias=None, residual=None, Z=None, stream=None):
+    """The layer with bias, activation and residual in its epilogue; Z
+    receives the pre-activation when it is given (C ABI qlin_forward_act)."""
+    f16, f32, n = torch.float16, torch.float32, M * w.N
+    _check(lib().qlin_forward_act(_buf(X, f16, M * w.K, "X"), M, ctypes.byref(w), _buf(s, f32, w.n_outlier, "s"),
+                                  float(gamma), int(bool(update_momentum)), act, _buf(bias, f32, w.N, "bias"),
+                                  _buf(residual, f16, n, "residual"), _buf(Z, f16, n, "Z"), _buf(Y, f16, n, "Y"),
+                                  _buf(workspace, torch.uint8, ws_bytes, "workspace"), ws_bytes, _stream(stream)),
+           "qlin_forward_act")
+
+
+def qlin_backward_act_workspace(M: int, w: qlin_weights) -> int:
+    return _size(lib().qlin_backward_act_workspace, M, ctypes.byref(w))
+
+
+def qlin_backward_act(w: qlin_weights, dY, Z, M: int, s, dX, dbias, workspace, ws_bytes: int,
+                      act: int = QLIN_ACT_NONE, stream=None):
+    """Input and bias gradients of qlin_forward_act (dX or dbias may be None)."""
+    f16, f32, n = torch.float16, torch.float32, M * w.N
+    _check(lib().qlin_backward_act(ctypes.byref(w), _buf(dY, f16, n, "dY"), _buf(Z, f16, n, "Z"), act, M,
+                                   _buf(s, f32, w.n_outlier, "s"), _buf(dX, f16, M * w.K, "dX"),
+                                   _buf(dbias, f32, w.N, "dbias"), _buf(workspace, torch.uint8, ws_bytes, "workspace"),
+                                   ws_bytes, _stream(stream)), "qlin_backward_act")
+
+
+def qlin_pack_gated(W_gate, W_up, O_host: np.ndarray, w: qlin_weights, stream=None):
+    """Pack gate and up projections [K][F] as one layer with alternating channels."""
+    O_host = np.ascontiguousarray(O_host, dtype=np.int32)
+    optr = O_host.ctypes.data if len(O_host) else None
+    n = w.K * (w.N // 2)
+    _check(lib().qlin_pack_gated(_buf(W_gate, torch.float16, n, "W_gate"), _buf(W_up, torch.float16, n, "W_up"), optr,
+                                 ctypes.byref(w), _stream(stream)), "qlin_pack_gated")
+
+
+def qlin_forward_gated_workspace(M: int, w: qlin_weights) -> int:
+    return _size(lib().qlin_forward_gated_workspace, M, ctypes.byref(w))
+
+
+def qlin_forward_gated(X, M: int, w: qlin_weights, s, gamma: float, update_momentum: bool, H, workspace, ws_bytes: int,
+                       act: int = QLIN_ACT_SILU, bias=None, Z=None, stream=None):
+    """act(gate) * up of a layer packed by qlin_pack_gated, in one GEMM
+    (C ABI qlin_forward_gated); bias and Z are in the packed order."""
+    f16, f32, n = torch.float16, torch.float32, M * w.N
+    _check(lib().qlin_forward_gated(_buf(X, f16, M * w.K, "X"), M, ctypes.byref(w), _buf(s, f32, w.n_outlier, "s"),
+                                    float(gamma), int(bool(update_momentum)), act, _buf(bias, f32, w.N, "bias"),
+                                    _buf(Z, f16, n, "Z"), _buf(H, f16, n // 2, "H"),
+                                    _buf(workspace, torch.uint8, ws_bytes, "workspace"), ws_bytes, _stream(stream)),
+           "qlin_forward_gated")
+
+
+def qlin_backward_gated_workspace(M: int, w: qlin_weights) -> int:
+    return _size(lib().qlin_backward_gated_workspace, M, ctypes.byref(w))
+
+
+def qlin_backward_gated(w: qlin_weights, dH, Z, M: int, s, dX, dbias, workspace, ws_bytes: int,
+                        act: int = QLIN_ACT_SILU, stream=None):
+    """Input and bias gradients of qlin_forward_gated (dX or dbias may be None)."""
+    f16, f32, n = torch.float16, torch.float32, M * w.N
+    _check(lib().qlin_backward_gated(ctypes.byref(w), _buf(dH, f16, n // 2, "dH"), _buf(Z, f16, n, "Z"), act, M,
+                                     _buf(s, f32, w.n_outlier, "s"), _buf(dX, f16, M * w.K, "dX"),
+                                     _buf(dbias, f32, w.N, "dbias"),
+                                     _buf(workspace, torch.uint8, ws_bytes, "workspace"), ws_bytes, _stream(stream)),
+           "qlin_backward_gated")
+
+
+def qlin_norm_forward(X, M: int, K: int, kind: int, gamma, beta, eps: float, Y, mean=None, rstd=None, stream=None):
+    """Layer norm or RMS norm of the rows of X; mean and rstd are kept for the
+    backward pass when given."""
+    f16, f32 = torch.float16, torch.float32
+    _check(lib().qlin_norm_forward(_buf(X, f16, M * K, "X"), M, K, kind, _buf(gamma, f32, K, "gamma"),
+                                   _buf(beta, f32, K, "beta"), float(eps), _buf(Y, f16, M * K, "Y"),
+                                   _buf(mean, f32, M, "mean"), _buf(rstd, f32, M, "rstd"), _stream(stream)),
+           "qlin_norm_forward")
+
+
+def qlin_norm_backward_workspace(M: int, K: int) -> int:
+    return _size(lib().qlin_norm_backward_workspace, M, K)
+
+
+def qlin_norm_backward(dY, X, M: int, K: int, kind: int, gamma, mean, rstd, dres, dX, dgamma, dbeta, workspace=None,
+                       ws_bytes: int = 0, stream=None):
+    """Gradients of qlin_norm_forward; dres (or None) is added to dX; dX,
+    dgamma and dbeta may each be None."""
+    f16, f32 = torch.float16, torch.float32
+    _check(lib().qlin_norm_backward(_buf(dY, f16, M * K, "dY"), _buf(X, f16, M * K, "X"), M, K, kind,
+                                    _buf(gamma, f32, K, "gamma"), _buf(mean, f32, M, "mean"),
+                                    _buf(rstd, f32, M, "rstd"), _buf(dres, f16, M * K, "dres"),
+                                    _buf(dX, f16, M * K, "dX"), _buf(dgamma, f32, K, "dgamma"),
+                                    _buf(dbeta, f32, K, "dbeta"), _buf(workspace, torch.uint8, ws_bytes, "workspace"),
+                                    ws_bytes, _stream(stream)), "qlin_norm_backward")
+
+
 def qlin_debug_set(knob: int, value: int) -> int:
     """Set a test/measurement knob; returns its previous value."""
     prev = ctypes.c_int64(0)
@@ -392,6 +530,16 @@ class PackedLayer:
         K, N = W.shape
         layer = cls(K, N, fmt, len(O), device=W.device)
         qlin_pack_weights(W, O, layer.w, stream)
+        return layer
+
+    @classmethod
+    def pack_gated(cls, W_gate: torch.Tensor, W_up: torch.Tensor, O: np.ndarray, fmt: int, stream=None) -> "PackedLayer":
+        """Gate and up projections [K][F] as one layer of 2 F alternating channels."""
+        if W_gate.shape != W_up.shape:
+            raise ValueError(f"gate {tuple(W_gate.shape)} and up {tuple(W_up.shape)} differ")
+        K, F = W_gate.shape
+        layer = cls(K, 2 * F, fmt, len(O), device=W_gate.device)
+        qlin_pack_gated(W_gate, W_up, O, layer.w, stream)
         return layer
 
     def clone(self) -> "PackedLayer":
