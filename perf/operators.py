@@ -190,6 +190,24 @@ def _own_norm(s):
     s["ws"] = qlin.empty_workspace(s["nws"])
 
 
+def _same_codes(layer, B, fmt):
+    """Lays the case's own weight codes out in the packed layer (the tiles of include/qlin.h): a weight that lies
+    on the border between two codes may fall on either side of it in the packer."""
+    if fmt == G128:  # quantized by divisions that round alike on both sides
+        return
+    (K, N), r = B.shape, torch.arange(128, device=B.device)[:, None]
+    TN, KB = -(-N // 128), -(-K // 128)
+    full = torch.zeros(TN * 128, KB * 128, dtype=torch.int8, device=B.device)
+    full[:N, :K] = B.t()
+    x = full.view(TN, 128, KB, 128).permute(0, 2, 1, 3)
+    if fmt == PC:  # byte b of a word: input b in the low nibble, input 4 + b in the high one
+        q = (x.reshape(TN, KB, 128, 16, 2, 4) >> 4) & 15
+        x = (q[..., 0, :] | (q[..., 1, :] << 4)).reshape(TN, KB, 128, 64)
+    n = x.shape[-1] // 16
+    at = torch.arange(n, device=B.device) ^ ((r >> 1) & 3 if fmt == PC else r & 7)
+    layer.view("codes").copy_(x.reshape(TN, KB, 128, n, 16)[:, :, r, at].reshape(-1).view(torch.uint8))
+
+
 def _own_weights(s):
     from quantized_linear_layers_token_b200 import qlin
     case, M = s["case"], s["case"]["M"]
@@ -198,6 +216,7 @@ def _own_weights(s):
         s["layer"] = qlin.PackedLayer.pack_gated(s["W"][:, 0::2].contiguous(), s["W"][:, 1::2].contiguous(), O, case["fmt"])
     else:
         s["layer"] = qlin.PackedLayer.pack(s["W"], O, case["fmt"])
+    _same_codes(s["layer"], s["B"], case["fmt"])
     w, N = s["layer"].w, s["layer"].N
     s["q"], s["act"] = qlin, ACTS.index(case["act"])
     if case["op"].endswith("_bwd"):
