@@ -350,9 +350,8 @@ QLIN_API qlin_status qlin_forward_act(const uint16_t* X, int32_t M, const qlin_w
  *   dX     device fp16 [M][K], fully overwritten, or NULL; dbias device fp32
  *          [N], fully overwritten, or NULL; at least one of them is wanted.
  *   s      as in qlin_backward_dx.
- *   workspace  qlin_backward_act_workspace bytes, 256-byte aligned; it must
- *          be zero-filled before its first use and is left that way where it
- *          has to be.
+ *   workspace  qlin_backward_act_workspace bytes, 256-byte aligned; no
+ *          zero-fill needed.
  * Arithmetic: dZ is formed in fp32 and rounded to fp16 once, multiplied by
  * the mantissa of c'_n and by a power of two of its row that keeps it in
  * range whatever the gradients' scale; the outlier rows of Weff are rounded

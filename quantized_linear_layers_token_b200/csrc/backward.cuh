@@ -63,24 +63,7 @@ struct BwdArgs {
   int tsplit;
   float* part;
   unsigned* cnt;
-  const float* rowscale;  // PRE kernels: factor of each token row [M]
 };
-
-// PRE kernels (the fused layers' backward pass): dY arrives as
-// dY[m][n] m_n 2^(e_m), c'_n = m_n p_n with p_n a power of two, so the
-// operand p_n B is exact in fp16 and the product's only roundings are those
-// of dY's scaled values, the outlier rows and dX itself.  p_n keeps
-// 127 p_n inside fp16's normal range; m_n takes what is left (in [1, 2)
-// unless c'_n is outside [2^-14, 2^9)).
-__device__ __forceinline__ float chan_pow2(float c) {
-  const int e = static_cast<int>((__float_as_uint(c) >> 23) & 0xFFu);  // biased exponent
-  const int k = e < 113 ? 113 : (e > 135 ? 135 : e);                   // 2^-14 .. 2^8
-  return __uint_as_float(static_cast<uint32_t>(k) << 23);
-}
-__device__ __forceinline__ float chan_mant(float c) {  // m_n = c'_n / p_n (exact)
-  const uint32_t k = __float_as_uint(chan_pow2(c)) >> 23;
-  return __fmul_rn(c, __uint_as_float((254u - k) << 23));
-}
 
 template <int FMT>
 struct BwdCfg {
@@ -216,19 +199,13 @@ __device__ __forceinline__ __half* outlier_elem(unsigned char* bt, int kl, int q
                                    ((((kl & 63) >> 3) ^ (q & 7)) << 4) + (kl & 7) * 2);
 }
 
-__device__ __forceinline__ void patch_outlier(unsigned char* bt, const float4 o, int q, float w) {
+__device__ __forceinline__ void patch_outlier(unsigned char* bt, const float4 o, int q, uint16_t w) {
   __half* p = outlier_elem(bt, __float_as_int(o.x), q);
-  const float v = __fmul_rn(__fmaf_rn(o.z, w, __half2float(*p)), o.w);
+  const float v = __fmul_rn(__fmaf_rn(o.z, __half2float(__ushort_as_half(w)), __half2float(*p)), o.w);
   *p = __float2half_rn(v);
 }
 
-// c'_n of the forward's INT8 operand: c_n / 16 for per-channel INT4 (16 q), else c_n.
 template <int FMT>
-__device__ __forceinline__ float bwd_chan(float c) {
-  return FMT == kFmtW4PC ? __fmul_rn(c, 0.0625f) : c;
-}
-
-template <int FMT, bool PRE>
 __global__ void __launch_bounds__(BwdCfg<FMT>::kThreads, 1)
 backward_dx_kernel(const __grid_constant__ CUtensorMap tmDY, const __grid_constant__ BwdArgs args) {
   using C = BwdCfg<FMT>;
@@ -423,8 +400,8 @@ backward_dx_kernel(const __grid_constant__ CUtensorMap tmDY, const __grid_consta
       }
       unsigned char* bt = smem + C::kOffB + b * C::kBBytes;
       unsigned char* brow = bt + (nl >> 3) * kBwdSbo + sw * 128;
-      const float cp = bwd_chan<FMT>(in.c);
-      const __half2 c2 = __float2half2_rn(PRE ? chan_pow2(cp) : cp);
+      // c'_n of the forward's INT8 operand: c_n / 16 for per-channel INT4 (16 q), else c_n
+      const __half2 c2 = __float2half2_rn(FMT == kFmtW4PC ? __fmul_rn(in.c, 0.0625f) : in.c);
       if (FMT == kFmtW8) {
         // two 16-input chunks of the code block's 128-byte row
 #pragma unroll
@@ -489,13 +466,7 @@ backward_dx_kernel(const __grid_constant__ CUtensorMap tmDY, const __grid_consta
             uint16_t w;
             if (e < ne) w = reinterpret_cast<const uint16_t*>(ring + q * C::kWRow)[lo8 + e];
             else w = wot_elem(args, j * 64 + q, __float_as_int(o.y));
-            float wf = __half2float(__ushort_as_half(w));
-            if (PRE) {  // in units of m_n; a channel without a scale has only zero weights
-              const int n = j * 64 + q;
-              const float m = n < args.N ? chan_mant(bwd_chan<FMT>(__ldg(args.cscale + n))) : 0.f;
-              wf = m > 0.f ? __fdiv_rn(wf, m) : 0.f;
-            }
-            patch_outlier(bt, o, q, wf);
+            patch_outlier(bt, o, q, w);
           }
         }
       }
@@ -532,24 +503,13 @@ backward_dx_kernel(const __grid_constant__ CUtensorMap tmDY, const __grid_consta
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
     };
-    float rsc[2] = {1.f, 1.f};  // PRE: the factors of this thread's rows
-    if (PRE) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int m = m0 + h * 128 + qd * 32 + lane;
-        if (m < args.M) rsc[h] = args.rowscale[m];
-      }
-    }
     auto store_dx = [&](int row, int col, const float (&v)[16]) {
       const int m = m0 + row;
       const int k = k0 + col;
       if (m < args.M && k < args.K) {
-        const float f = PRE ? (row < 128 ? rsc[0] : rsc[1]) : 1.f;
         uint32_t hw[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          hw[e] = PRE ? h2_as_u32(__floats2half2_rn(__fmul_rn(v[2 * e], f), __fmul_rn(v[2 * e + 1], f)))
-                      : h2_as_u32(__floats2half2_rn(v[2 * e], v[2 * e + 1]));
+        for (int e = 0; e < 8; ++e) hw[e] = h2_as_u32(__floats2half2_rn(v[2 * e], v[2 * e + 1]));
         uint4* dst = reinterpret_cast<uint4*>(args.dX + static_cast<size_t>(m) * args.K + k);
         dst[0] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
         dst[1] = make_uint4(hw[4], hw[5], hw[6], hw[7]);

@@ -8,14 +8,14 @@
 //   dbias_n = sum_m dZ[m][n]
 //
 // The product runs on the fp16 tensor cores, so dZ is rounded to fp16 once.
-// It is written as dZ m_n 2^(e_m) (backward.cuh: m_n the mantissa of the
+// It is written as dZ m_n 2^(e_m) (dx_pair.cuh: m_n the mantissa of the
 // channel scale): the power of two of each row puts the largest |dZ| the row
 // can hold near 2^14, so neither a large gradient times a large up value
 // overflows nor a small one loses digits, whatever the scale of the loss; the
 // product undoes it in fp32.  The bias's gradient sums the fp32 dZ.
 #pragma once
 
-#include "backward.cuh"
+#include "dx_pair.cuh"
 #include "norm.cuh"
 
 namespace qlin {

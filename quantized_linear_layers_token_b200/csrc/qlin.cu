@@ -18,6 +18,7 @@
 #include "gemm_pair.cuh"
 #include "backward.cuh"
 #include "dact.cuh"
+#include "dx_pair.cuh"
 #include "gptq.cuh"
 #include "norm.cuh"
 #include "offq.cuh"
@@ -991,10 +992,10 @@ BwdPlan plan_backward(int M, const qlin_weights* w, bool split) {
   return p;
 }
 
-template <int FMT, bool PRE>
+template <int FMT>
 qlin_status launch_backward_t(const CUtensorMap& tm, const BwdArgs& args, cudaStream_t stream) {
   using C = BwdCfg<FMT>;
-  auto kern = backward_dx_kernel<FMT, PRE>;
+  auto kern = backward_dx_kernel<FMT>;
   static std::once_flag attr_once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(attr_once, [&] {
@@ -1005,49 +1006,6 @@ qlin_status launch_backward_t(const CUtensorMap& tm, const BwdArgs& args, cudaSt
   cudaError_t e = launch_k(kern, grid, dim3(C::kThreads), C::kSmemBytes, stream, tm, args);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "backward_dx_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
-}
-
-// The input gradient's launch.  PRE: dY holds the scaled gradients of
-// dact.cuh and `rowscale` the factors that undo their rows' scales.
-template <bool PRE>
-qlin_status launch_backward(const qlin_weights* w, const uint16_t* dY, int M, const float* s, uint16_t* dX,
-                            const float* rowscale, void* workspace, size_t ws_bytes, cudaStream_t stream) {
-  qlin_status st = get_encoder();
-  if (st != QLIN_OK) return st;
-  CUtensorMap tm;
-  st = make_map(&tm, dY, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->N, M, 64, 256, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st != QLIN_OK) return st;
-  const int nO = w->n_outlier;
-  BwdArgs args;
-  args.codes = static_cast<const uint8_t*>(w->codes);
-  args.rfold = w->fold_ratio;
-  args.wot = w->W_Ot;
-  args.cscale = w->chan_scale;
-  args.oidx = w->outlier_idx;
-  args.s = s;
-  args.dX = dX;
-  args.M = M;
-  args.N = w->N;
-  args.K = w->K;
-  args.nO = nO;
-  args.rowscale = rowscale;
-  args.kbs = (w->K + 127) / 128;
-  args.nib = (nO + 63) / 64;
-  args.nsteps = (w->N + 63) / 64;
-  // the split plan needs the whole workspace it asks for; with none (or a
-  // smaller one) every tile runs whole
-  BwdPlan p = plan_backward(M, w, true);
-  if (p.bytes && (!workspace || ws_bytes < p.bytes)) p = plan_backward(M, w, false);
-  args.ntk = p.ntk;
-  args.full = p.full;
-  args.tsplit = p.tsplit;
-  args.part = p.bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_off) : nullptr;
-  args.cnt = p.bytes ? reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + p.cnt_off) : nullptr;
-  switch (w->fmt) {
-    case QLIN_W4_PERCHANNEL: return launch_backward_t<kFmtW4PC, PRE>(tm, args, stream);
-    case QLIN_W4_G128: return launch_backward_t<kFmtW4G128, PRE>(tm, args, stream);
-    default: return launch_backward_t<kFmtW8, PRE>(tm, args, stream);
-  }
 }
 
 // ---------------------------------------------------------------- packing
@@ -1146,23 +1104,134 @@ qlin_status launch_column_sum(const float* part, int G, int K, float* out0, floa
   return QLIN_OK;
 }
 
-// Workspace of a fused layer's backward pass: the scaled dZ, the rows'
-// factors, the bias gradient's partial sums, the input gradient's split
-// tiles (zero before the first use, left zero).
+// Work split of the fused layers' input gradient: 256 x 256 tiles on CTA
+// pairs, their reduction cut into S ranges when that shortens the longest
+// pair's work: a unit costs its steps (about 0.28 us each) and some eight
+// more for its pipeline's ends, a split the traffic of its partial sums.
+struct DxPlan {
+  int tiles_k, tiles_m, S, units, ncl, nst, gm;
+};
+
+int dx_max_clusters() {
+  static int n = -1;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    n = 0;
+    if (cudaFuncSetAttribute(dx_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DxCfg::kSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * ((sm_count() + 1) / 2)));
+    cfg.blockDim = dim3(DxCfg::kThreads);
+    cfg.dynamicSmemBytes = DxCfg::kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int c = 0;
+    if (cudaOccupancyMaxActiveClusters(&c, dx_pair_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      c = 0;
+    }
+    n = c;
+  });
+  return n;
+}
+
+DxPlan plan_dx(int M, const qlin_weights* w) {
+  DxPlan p{};
+  const int pairs = dx_max_clusters() > 0 ? dx_max_clusters() : 1;
+  p.tiles_k = (w->K + 255) / 256;
+  p.tiles_m = (M + 255) / 256;
+  p.nst = (w->N + 63) / 64;
+  const long long tiles = static_cast<long long>(p.tiles_k) * p.tiles_m;
+  double best = 0.0;
+  for (int S = 1; S <= 16 && S <= p.nst; ++S) {
+    const double waves = static_cast<double>((tiles * S + pairs - 1) / pairs);
+    const double traffic = S > 1 ? 8.0 * S * M * w->K / 1.7e6 + 10.0 : 0.0;  // bytes over about 6 TB/s, in steps
+    const double cost = waves * ((p.nst + S - 1) / S + 8.0) + traffic;
+    if (S == 1 || cost < best) {
+      best = cost;
+      p.S = S;
+    }
+  }
+  const long long units = tiles * p.S;
+  p.units = static_cast<int>(units);
+  p.ncl = static_cast<int>(units < pairs ? units : pairs);
+  p.gm = p.tiles_m < 9 ? p.tiles_m : 9;
+  return p;
+}
+
+// Workspace of a fused layer's backward pass: the widened weight operand, the
+// scaled dZ, the rows' factors, the partial sums of split tiles and of the
+// bias's gradient.
 struct FusedBwdLayout {
-  size_t split, dz, rows, part, total;
+  size_t wide, dz, rows, dxpart, part, total;
+  DxPlan dx;
   int G;
 };
 FusedBwdLayout fused_bwd_layout(int M, const qlin_weights* w) {
   FusedBwdLayout L{};
+  L.dx = plan_dx(M, w);
   size_t off = 0;
-  L.split = off; off = round_up(off + plan_backward(M, w, true).bytes, kAlign);
+  L.wide = off; off = round_up(off + size_t((w->K + 127) / 128) * L.dx.nst * 16384, kAlign);
   L.dz = off; off = round_up(off + size_t(M) * w->N * 2, kAlign);
   L.rows = off; off = round_up(off + size_t(M) * 4, kAlign);
+  L.dxpart = off; off = round_up(off + (L.dx.S > 1 ? size_t(L.dx.S) * M * w->K * 4 : 0), kAlign);
   L.G = column_groups(M, w->N / 8);
   L.part = off; off = round_up(off + size_t(L.G) * w->N * 4, kAlign);
   L.total = off;
   return L;
+}
+
+template <int FMT>
+cudaError_t launch_dx_widen(const DxWidenArgs& a, int tiles_n, cudaStream_t stream) {
+  return launch_k(dx_widen_kernel<FMT>, dim3(static_cast<unsigned>(tiles_n) * static_cast<unsigned>(a.kb)), dim3(256), 0,
+                  stream, a);
+}
+
+// dX from the scaled dZ and the widened operand.
+qlin_status launch_dx(const qlin_weights* w, int M, const FusedBwdLayout& L, char* ws, uint16_t* dX, cudaStream_t stream) {
+  qlin_status st = get_encoder();
+  if (st != QLIN_OK) return st;
+  if (dx_max_clusters() < 1) return fail(QLIN_ERR_CUDA, "dx_pair_kernel: no 2-CTA cluster fits");
+  const DxPlan& p = L.dx;
+  const uint64_t kb = (w->K + 127) / 128;
+  DxParams prm;
+  memset(&prm, 0, sizeof(prm));
+  DxArgs& g = prm.g;
+  g.rowscale = reinterpret_cast<const float*>(ws + L.rows);
+  g.dX = dX;
+  g.part = reinterpret_cast<float*>(ws + L.dxpart);
+  g.M = M;
+  g.K = w->K;
+  g.nst = p.nst;
+  g.tiles_k = p.tiles_k;
+  g.tiles_m = p.tiles_m;
+  g.S = p.S;
+  g.units = p.units;
+  g.ncl = p.ncl;
+  g.gm = p.gm;
+  st = make_map(&prm.tmA, ws + L.dz, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->N, M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != QLIN_OK) return st;
+  st = make_map(&prm.tmB, ws + L.wide, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, kb * p.nst * 128, 128, 128,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (st != QLIN_OK) return st;
+  st = make_map(&prm.tmX, dX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->K, M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != QLIN_OK) return st;
+  cudaError_t e = launch_kc(dx_pair_kernel, dim3(static_cast<unsigned>(2 * p.ncl)), dim3(DxCfg::kThreads), DxCfg::kSmem,
+                            stream, 2, prm);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dx_pair_kernel launch failed: %s", cudaGetErrorString(e));
+  if (p.S > 1) {
+    const size_t blocks = (size_t(M) * w->K / 8 + 255) / 256;
+    e = launch_k(dx_reduce_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, g);
+    if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dx_reduce_kernel launch failed: %s", cudaGetErrorString(e));
+  }
+  return QLIN_OK;
 }
 
 template <bool GATED>
@@ -1182,6 +1251,8 @@ qlin_status backward_fused(const qlin_weights* w, const uint16_t* dY, const uint
   }
   const int nO = w->n_outlier;
   const bool needs_z = GATED || act != QLIN_ACT_NONE;
+  if (size_t((w->K + 127) / 128) * ((w->N + 63) / 64) * 128 >= size_t(1) << 31)
+    return fail(QLIN_ERR_SHAPE, "K=%d N=%d: the widened weights exceed 2^31 rows of 128 bytes", w->K, w->N);
   if (!dX && !dbias) return fail(QLIN_ERR_ARG, "dX and dbias are both NULL");
   if (!dY || (needs_z && !Z)) return fail(QLIN_ERR_ARG, "dY/Z is NULL");
   if (nO > 0 && dX && !s) return fail(QLIN_ERR_ARG, "s is NULL with n_outlier=%d", nO);
@@ -1212,7 +1283,25 @@ qlin_status backward_fused(const qlin_weights* w, const uint16_t* dY, const uint
   if (!dX) return QLIN_OK;
   cudaError_t e = launch_k(dact_rows_kernel<GATED>, dim3(static_cast<unsigned>(M)), dim3(kDactThreads), 0, stream, g);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_rows_kernel launch failed: %s", cudaGetErrorString(e));
-  return launch_backward<true>(w, g.dZ, M, s, dX, g.rowscale, ws + L.split, L.dz - L.split, stream);
+  DxWidenArgs a{};
+  a.codes = static_cast<const uint8_t*>(w->codes);
+  a.rfold = w->fold_ratio;
+  a.wot = w->W_Ot;
+  a.cscale = w->chan_scale;
+  a.oidx = w->outlier_idx;
+  a.s = s;
+  a.out = reinterpret_cast<uint8_t*>(ws + L.wide);
+  a.N = w->N;
+  a.nO = nO;
+  a.kb = (w->K + 127) / 128;
+  a.nst = L.dx.nst;
+  a.nib = (nO + 63) / 64;
+  const int tiles_n = (w->N + 127) / 128;
+  e = w->fmt == QLIN_W4_PERCHANNEL ? launch_dx_widen<kFmtW4PC>(a, tiles_n, stream)
+      : w->fmt == QLIN_W4_G128     ? launch_dx_widen<kFmtW4G128>(a, tiles_n, stream)
+                                   : launch_dx_widen<kFmtW8>(a, tiles_n, stream);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dx_widen_kernel launch failed: %s", cudaGetErrorString(e));
+  return launch_dx(w, M, L, ws, dX, stream);
 }
 
 qlin_status check_norm(int32_t M, int32_t K, int32_t kind) {
@@ -1458,7 +1547,41 @@ qlin_status qlin_backward_dx(const qlin_weights* w, const uint16_t* dY, int32_t 
   if (nO > 0 && !s) return fail(QLIN_ERR_ARG, "s is NULL with n_outlier=%d", nO);
   if (!aligned16(dY) || !aligned16(dX) || (s && !aligned16(s)))
     return fail(QLIN_ERR_ALIGN, "a backward buffer is not 16-byte aligned");
-  return launch_backward<false>(w, dY, M, s, dX, nullptr, workspace, ws_bytes, static_cast<cudaStream_t>(stream_));
+  st = get_encoder();
+  if (st != QLIN_OK) return st;
+  CUtensorMap tm;
+  st = make_map(&tm, dY, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->N, M, 64, 256, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != QLIN_OK) return st;
+  BwdArgs args;
+  args.codes = static_cast<const uint8_t*>(w->codes);
+  args.rfold = w->fold_ratio;
+  args.wot = w->W_Ot;
+  args.cscale = w->chan_scale;
+  args.oidx = w->outlier_idx;
+  args.s = s;
+  args.dX = dX;
+  args.M = M;
+  args.N = w->N;
+  args.K = w->K;
+  args.nO = nO;
+  args.kbs = (w->K + 127) / 128;
+  args.nib = (nO + 63) / 64;
+  args.nsteps = (w->N + 63) / 64;
+  // the split plan needs the whole workspace it asks for; with none (or a
+  // smaller one) every tile runs whole
+  BwdPlan p = plan_backward(M, w, true);
+  if (p.bytes && (!workspace || ws_bytes < p.bytes)) p = plan_backward(M, w, false);
+  args.ntk = p.ntk;
+  args.full = p.full;
+  args.tsplit = p.tsplit;
+  args.part = p.bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_off) : nullptr;
+  args.cnt = p.bytes ? reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + p.cnt_off) : nullptr;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  switch (w->fmt) {
+    case QLIN_W4_PERCHANNEL: return launch_backward_t<kFmtW4PC>(tm, args, stream);
+    case QLIN_W4_G128: return launch_backward_t<kFmtW4G128>(tm, args, stream);
+    default: return launch_backward_t<kFmtW8>(tm, args, stream);
+  }
 }
 
 qlin_status qlin_forward_workspace(int32_t M, const qlin_weights* w, size_t* bytes) {
