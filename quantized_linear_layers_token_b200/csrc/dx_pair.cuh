@@ -91,17 +91,20 @@ __global__ void __launch_bounds__(256) dx_widen_kernel(const __grid_constant__ D
     rb[i] = (FMT == kFmtW4G128 && n < g.N) ? __ldg(g.rfold + static_cast<size_t>(kb) * g.N + n) : uint16_t(0);
   }
   griddep_wait();  // s comes from the forward; the workspace may still be read
+  // which inputs of the block are outliers: the whole list read at once (a
+  // binary search is a chain of dependent loads: 10 us a block)
   int nout = 0;
   if (g.nO > 0) {
-    const int lo = lower_bound_i32(g.oidx, g.nO, kb * 128);
-    nout = lower_bound_i32(g.oidx, g.nO, kb * 128 + 128) - lo;
-    if (nout > 0) {
-      if (threadIdx.x < 128) orow[threadIdx.x] = -1;
-      __syncthreads();
-      if (static_cast<int>(threadIdx.x) < nout)
-        orow[__ldg(g.oidx + lo + threadIdx.x) - kb * 128] = static_cast<int16_t>(lo + threadIdx.x);
-      __syncthreads();
+    if (threadIdx.x < 128) orow[threadIdx.x] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < g.nO; i += 256) {
+      const int k = __ldg(g.oidx + i) - kb * 128;
+      if (k >= 0 && k < 128) {
+        orow[k] = static_cast<int16_t>(i);
+        nout = 1;
+      }
     }
+    nout = __syncthreads_or(nout);
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {

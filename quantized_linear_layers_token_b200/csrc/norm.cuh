@@ -15,6 +15,7 @@
 // so results repeat bit for bit.
 #pragma once
 
+#include "gemm.cuh"
 #include "pack.cuh"
 
 namespace qlin {
@@ -182,12 +183,12 @@ __global__ void __launch_bounds__(128) norm_columns_kernel(const __grid_constant
   pb[1] = make_float4(sb[4], sb[5], sb[6], sb[7]);
 }
 
-// out[k] = sum over the G partial rows, in one order: eight warps take the
-// rows w, w + 8, ... of 32 columns, and their sums are added in order.
+// out[k] = sum over the G partial rows, in one order: 32 warps take the rows
+// w, w + 32, ... of 32 columns, and their sums are added in order.
 // blockIdx.y selects dgamma (0) or dbeta (1).
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part, int G, int K,
-                                                         float* __restrict__ out0, float* __restrict__ out1) {
-  __shared__ float red[8][32];
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part, int G, int K,
+                                                          float* __restrict__ out0, float* __restrict__ out1) {
+  __shared__ float red[32][33];
   griddep_launch_dependents();
   griddep_wait();
   float* out = blockIdx.y ? out1 : out0;
@@ -198,14 +199,267 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
   float s = 0.f;
   if (k < K) {
 #pragma unroll 8
-    for (int i = w; i < G; i += 8) s += p[static_cast<size_t>(i) * K];
+    for (int i = w; i < G; i += 32) s += p[static_cast<size_t>(i) * K];
   }
   red[w][c] = s;
   __syncthreads();
-  if (w == 0 && k < K) {
+  // warp w adds the 32 sums of column w, a lane each
+  s = warp_sum(red[c][w]);
+  if (c == 0 && static_cast<int>(blockIdx.x) * 32 + w < K) out[blockIdx.x * 32 + w] = s;
+}
+
+// ---- Row rings: persistent CTAs of T threads work through the rows
+// blockIdx.x, + gridDim.x, ...; one thread keeps the next kRingStages rows on
+// their way into shared memory with bulk copies, so the loads do not wait for
+// the row in hand and need no registers.  Thread t owns the 8-element
+// vectors t, t + T, ... of every row, VPT of them at most.
+constexpr int kRingStages = 3;
+
+// The next row of a stage: `n` arrays of `bytes` each, one after the other.
+__device__ __forceinline__ void ring_load(unsigned char* dst, const uint16_t* a, const uint16_t* b, const uint16_t* c,
+                                          size_t row, int K, uint64_t* bar) {
+  const uint32_t bytes = static_cast<uint32_t>(K) * 2u;
+  mbar_arrive_expect_tx(bar, bytes * (1u + (b ? 1u : 0u) + (c ? 1u : 0u)));
+  bulk_load(dst, a + row * K, bytes, bar);
+  if (b) bulk_load(dst + bytes, b + row * K, bytes, bar);
+  if (c) bulk_load(dst + 2 * bytes, c + row * K, bytes, bar);
+}
+
+// Shared memory of a ring: the stages of `rows` rows of K values.
+__host__ __device__ inline size_t ring_bytes(int K, int rows) { return size_t(kRingStages) * rows * K * 2; }
+
+// Forward over a ring.  gamma and beta stay in registers (VPT <= 2).
+template <int T, int VPT>
+__global__ void __launch_bounds__(T) norm_forward_ring_kernel(const __grid_constant__ NormFwdArgs g) {
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ float red[2][2][32];
+  __shared__ uint64_t full[kRingStages];
+  __shared__ int abort_flag;
+  const int t = threadIdx.x;
+  const int nv = g.K >> 3;
+  const size_t stage = static_cast<size_t>(g.K) * 2;
+  if (t == 0) {
+    for (int s = 0; s < kRingStages; ++s) mbar_init(&full[s], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+  const int step = static_cast<int>(gridDim.x);
+  int issued = 0;  // rows on their way (thread 0)
+  if (t == 0) {
+    for (int s = 0; s < kRingStages; ++s) {
+      const size_t m = blockIdx.x + static_cast<size_t>(s) * step;
+      if (m < static_cast<size_t>(g.M)) {
+        ring_load(ring_smem + s * stage, g.X, nullptr, nullptr, m, g.K, &full[s]);
+        ++issued;
+      }
+    }
+  }
+  float gm[VPT][8], bt[VPT][8];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][c];
-    out[k] = s;
+  for (int j = 0; j < VPT; ++j) {
+    const int v = t + j * T;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gm[j][e] = bt[j][e] = 0.f;
+    if (v < nv) {
+      load_f8(g.gamma + 8 * v, gm[j]);
+      if (g.beta) load_f8(g.beta + 8 * v, bt[j]);
+    }
+  }
+  const float invk = 1.f / static_cast<float>(g.K);
+  int i = 0;
+  for (size_t m = blockIdx.x; m < static_cast<size_t>(g.M); m += step, ++i) {
+    const int s = i % kRingStages;
+    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / kRingStages) & 1u, &abort_flag)) abort_flag = 1;
+    const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
+    uint4 x[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) x[j] = t + j * T < nv ? xr[t + j * T] : make_uint4(0u, 0u, 0u, 0u);
+    float mu = 0.f;
+    if (!g.rms) {
+      float a = 0.f;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        float f[8];
+        h8_to_f(x[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a += f[e];
+      }
+      mu = row_sum<T>(a, red[i & 1][0]) * invk;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (t + j * T < nv) {
+        float f[8];
+        h8_to_f(x[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(f[e] - mu, f[e] - mu, q);
+      }
+    }
+    const float r = 1.f / sqrtf(fmaf(row_sum<T>(q, red[i & 1][1]), invk, g.eps));
+    // every thread holds its part of the row (the sum's barrier): refill
+    if (t == 0) {
+      const size_t next = m + static_cast<size_t>(kRingStages) * step;
+      if (abort_flag == 0 && next < static_cast<size_t>(g.M)) {
+        ring_load(ring_smem + s * stage, g.X, nullptr, nullptr, next, g.K, &full[s]);
+        ++issued;
+      }
+      if (g.mean) g.mean[m] = mu;
+      if (g.rstd) g.rstd[m] = r;
+    }
+    uint4* yr = reinterpret_cast<uint4*>(g.Y + m * g.K);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (t + j * T < nv) {
+        float f[8];
+        h8_to_f(x[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mu) * r, gm[j][e], bt[j][e]);
+        yr[t + j * T] = f_to_h8(f);
+      }
+    }
+  }
+  if (t == 0 && abort_flag) drain_ring(full, kRingStages, issued);  // no copy outlives the CTA
+}
+
+// Backward over a ring: dX, and with ACC the column sums of dy xh and dy over
+// the CTA's rows in registers, written once as partial row blockIdx.x.  Each
+// row costs one barrier: its two sums are taken together.  A stage is
+// refilled after the next row's barrier, when every thread is done with it.
+template <int T, int VPT, bool ACC>
+__global__ void __launch_bounds__(T) norm_backward_ring_kernel(const __grid_constant__ NormBwdArgs g) {
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ float red[2][2][32];
+  __shared__ uint64_t full[kRingStages];
+  __shared__ int abort_flag;
+  const int t = threadIdx.x;
+  const int nv = g.K >> 3;
+  const size_t row_bytes = static_cast<size_t>(g.K) * 2;
+  const size_t stage = row_bytes * (g.dres ? 3 : 2);
+  if (t == 0) {
+    for (int s = 0; s < kRingStages; ++s) mbar_init(&full[s], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+  const size_t step = gridDim.x, M = static_cast<size_t>(g.M);
+  int issued = 0;  // rows on their way (thread 0)
+  if (t == 0) {
+    for (int s = 0; s < kRingStages; ++s) {
+      const size_t m = blockIdx.x + s * step;
+      if (m < M) {
+        ring_load(ring_smem + s * stage, g.dY, g.X, g.dres, m, g.K, &full[s]);
+        ++issued;
+      }
+    }
+  }
+  float sg[VPT][8], sb[VPT][8];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sg[j][e] = sb[j][e] = 0.f;
+  const float invk = 1.f / static_cast<float>(g.K);
+  float mu1 = 0.f, r1 = 0.f;  // the next row's statistics, loaded a row ahead
+  if (blockIdx.x < M) {
+    if (!g.rms) mu1 = g.mean[blockIdx.x];
+    r1 = g.rstd[blockIdx.x];
+  }
+  int i = 0;
+  for (size_t m = blockIdx.x; m < M; m += step, ++i) {
+    const int s = i % kRingStages;
+    const float mu = mu1, r = r1;
+    if (m + step < M) {
+      if (!g.rms) mu1 = g.mean[m + step];
+      r1 = g.rstd[m + step];
+    }
+    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / kRingStages) & 1u, &abort_flag)) abort_flag = 1;
+    const uint4* dr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
+    const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage + row_bytes);
+    const uint4* rr = reinterpret_cast<const uint4*>(ring_smem + s * stage + 2 * row_bytes);
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = t + j * T;
+      if (v < nv) {
+        float x[8], dy[8], gm[8];
+        h8_to_f(xr[v], x);
+        h8_to_f(dr[v], dy);
+        load_f8(g.gamma + 8 * v, gm);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float xh = (x[e] - mu) * r;
+          if (ACC) {
+            sg[j][e] = fmaf(dy[e], xh, sg[j][e]);
+            sb[j][e] += dy[e];
+          }
+          const float w = dy[e] * gm[e];
+          s1 += w;
+          s2 = fmaf(w, xh, s2);
+        }
+      }
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if ((t & 31) == 0) {
+      red[i & 1][0][t >> 5] = s1;
+      red[i & 1][1][t >> 5] = s2;
+    }
+    __syncthreads();
+    s1 = s2 = 0.f;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) {
+      s1 += red[i & 1][0][w];
+      s2 += red[i & 1][1][w];
+    }
+    s1 = g.rms ? 0.f : s1 * invk;
+    s2 *= invk;
+    if (t == 0 && i > 0 && abort_flag == 0) {  // the previous row's stage
+      const size_t next = m + static_cast<size_t>(kRingStages - 1) * step;
+      const int p = (i - 1) % kRingStages;
+      if (next < M) {
+        ring_load(ring_smem + p * stage, g.dY, g.X, g.dres, next, g.K, &full[p]);
+        ++issued;
+      }
+    }
+    if (g.dX) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v = t + j * T;
+        if (v < nv) {
+          float x[8], dy[8], gm[8], rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          h8_to_f(xr[v], x);
+          h8_to_f(dr[v], dy);
+          load_f8(g.gamma + 8 * v, gm);
+          if (g.dres) h8_to_f(rr[v], rs);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float xh = (x[e] - mu) * r;
+            x[e] = fmaf(r, dy[e] * gm[e] - s1 - xh * s2, rs[e]);
+          }
+          reinterpret_cast<uint4*>(g.dX + m * g.K)[v] = f_to_h8(x);
+        }
+      }
+    }
+  }
+  if (t == 0 && abort_flag) drain_ring(full, kRingStages, issued);  // no copy outlives the CTA
+  if (ACC) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = t + j * T;
+      if (v < nv) {
+        float4* pg = reinterpret_cast<float4*>(g.part + static_cast<size_t>(blockIdx.x) * g.K) + 2 * v;
+        float4* pb = reinterpret_cast<float4*>(g.part + (step + blockIdx.x) * g.K) + 2 * v;
+        pg[0] = make_float4(sg[j][0], sg[j][1], sg[j][2], sg[j][3]);
+        pg[1] = make_float4(sg[j][4], sg[j][5], sg[j][6], sg[j][7]);
+        pb[0] = make_float4(sb[j][0], sb[j][1], sb[j][2], sb[j][3]);
+        pb[1] = make_float4(sb[j][4], sb[j][5], sb[j][6], sb[j][7]);
+      }
+    }
   }
 }
 

@@ -1098,7 +1098,7 @@ int column_groups(int M, int nv) {
 // Partial column sums [G][K] (twice that, dgamma then dbeta, for a norm) to
 // their totals.
 qlin_status launch_column_sum(const float* part, int G, int K, float* out0, float* out1, cudaStream_t stream) {
-  cudaError_t e = launch_k(column_sum_kernel, dim3((K + 31) / 32, out1 ? 2 : 1), dim3(256), 0, stream, part, G, K, out0,
+  cudaError_t e = launch_k(column_sum_kernel, dim3((K + 31) / 32, out1 ? 2 : 1), dim3(1024), 0, stream, part, G, K, out0,
                            out1);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "column_sum_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
@@ -1317,14 +1317,64 @@ cudaError_t launch_norm_t(const NormFwdArgs& g, cudaStream_t stream) {
   return launch_k(norm_forward_kernel<T, VPT>, dim3(grid), dim3(T == 32 ? 128 : T), 0, stream, g);
 }
 
+// Rings of `rows` rows a stage: threads and vectors per thread of a row of K,
+// persistent CTAs per SM; ctas = 0 where the ring does not fit.
+struct RingPlan {
+  int threads, vpt, ctas;
+  size_t smem;
+};
+RingPlan ring_plan(int K, int rows) {
+  RingPlan p{};
+  const int nv = K / 8;
+  p.threads = nv <= 128 ? 128 : (nv <= 256 ? 256 : 512);
+  p.vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);
+  p.smem = ring_bytes(K, rows);
+  const int fit = static_cast<int>(size_t(220) * 1024 / p.smem);
+  const int most = p.vpt == 4 ? 1 : (p.threads == 512 ? 2 : 4);
+  p.ctas = nv > 2048 ? 0 : (fit < most ? fit : most);
+  return p;
+}
+
+template <typename Args>
+cudaError_t launch_ring(void (*kern)(Args), const RingPlan& p, unsigned grid, cudaStream_t stream, const Args& g) {
+  // raising a kernel's shared-memory limit is idempotent and needs no stream
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.smem));
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(grid), dim3(p.threads), p.smem, stream, g);
+}
+
+unsigned ring_grid(const RingPlan& p, int M) {
+  const int most = sm_count() * p.ctas;
+  return static_cast<unsigned>(M < most ? M : most);
+}
+
+template <bool ACC>
+cudaError_t launch_norm_backward_ring(const RingPlan& p, unsigned grid, const NormBwdArgs& g, cudaStream_t stream) {
+  if (p.threads == 128) return launch_ring(norm_backward_ring_kernel<128, 1, ACC>, p, grid, stream, g);
+  if (p.threads == 256) return launch_ring(norm_backward_ring_kernel<256, 1, ACC>, p, grid, stream, g);
+  if (p.vpt == 1) return launch_ring(norm_backward_ring_kernel<512, 1, ACC>, p, grid, stream, g);
+  if (p.vpt == 2) return launch_ring(norm_backward_ring_kernel<512, 2, ACC>, p, grid, stream, g);
+  return launch_ring(norm_backward_ring_kernel<512, 4, ACC>, p, grid, stream, g);
+}
+
+// Partial rows of dgamma and dbeta: one per CTA of the ring kernel, else one
+// per row group of the column kernel.  The workspace covers both (whether
+// dres is given decides whether a ring fits).
 struct NormBwdLayout {
-  int G;
+  RingPlan ring[2];  // without and with dres
+  int G;             // row groups of the column kernel
   size_t total;
 };
 NormBwdLayout norm_bwd_layout(int M, int K) {
   NormBwdLayout L{};
   L.G = column_groups(M, K / 8);
-  L.total = M > 0 ? round_up(size_t(2) * L.G * K * 4, kAlign) : 0;
+  int most = L.G;
+  for (int r = 0; r < 2; ++r) {
+    L.ring[r] = ring_plan(K, 2 + r);
+    const int n = static_cast<int>(ring_grid(L.ring[r], M));
+    if (n > most) most = n;
+  }
+  L.total = M > 0 ? round_up(size_t(2) * most * K * 4, kAlign) : 0;
   return L;
 }
 
@@ -1684,8 +1734,15 @@ qlin_status qlin_norm_forward(const uint16_t* X, int32_t M, int32_t K, int32_t k
   const NormFwdArgs g{X, gamma, beta, Y, kind == QLIN_NORM_RMS ? nullptr : mean, rstd, M, K, kind == QLIN_NORM_RMS, eps};
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const int nv = K / 8;
+  const RingPlan ring = ring_plan(K, 1);
   cudaError_t e;
-  if (nv <= 32) e = launch_norm_t<32, 1>(g, stream);
+  if (nv <= 1024 && M > sm_count() * ring.ctas) {  // more rows than one each for the persistent CTAs
+    const unsigned grid = ring_grid(ring, M);
+    if (ring.threads == 128) e = launch_ring(norm_forward_ring_kernel<128, 1>, ring, grid, stream, g);
+    else if (ring.threads == 256) e = launch_ring(norm_forward_ring_kernel<256, 1>, ring, grid, stream, g);
+    else if (ring.vpt == 1) e = launch_ring(norm_forward_ring_kernel<512, 1>, ring, grid, stream, g);
+    else e = launch_ring(norm_forward_ring_kernel<512, 2>, ring, grid, stream, g);
+  } else if (nv <= 32) e = launch_norm_t<32, 1>(g, stream);
   else if (nv <= 128) e = launch_norm_t<32, 4>(g, stream);
   else if (nv <= 512) e = launch_norm_t<128, 4>(g, stream);
   else if (nv <= 1024) e = launch_norm_t<256, 4>(g, stream);
@@ -1724,12 +1781,23 @@ qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M,
       (dres && !aligned16(dres)) || (dX && !aligned16(dX)))
     return fail(QLIN_ERR_ALIGN, "a norm buffer is not 16-byte aligned");
   NormBwdArgs g{dY, X, gamma, rms ? nullptr : mean, rstd, dres, dX, nullptr, M, K, rms, 0};
-  if (dgamma || dbeta) {
-    const NormBwdLayout L = norm_bwd_layout(M, K);
+  const NormBwdLayout L = norm_bwd_layout(M, K);
+  const RingPlan& ring = L.ring[dres ? 1 : 0];
+  const bool acc = dgamma || dbeta;
+  if (acc) {
     if (ws_bytes < L.total || !workspace) return fail(QLIN_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, L.total);
     if (reinterpret_cast<uintptr_t>(workspace) % kAlign)
       return fail(QLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
     g.part = static_cast<float*>(workspace);
+  }
+  if (ring.ctas > 0) {
+    const unsigned grid = ring_grid(ring, M);
+    cudaError_t e = acc ? launch_norm_backward_ring<true>(ring, grid, g, stream)
+                        : launch_norm_backward_ring<false>(ring, grid, g, stream);
+    if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "norm_backward_ring_kernel launch failed: %s", cudaGetErrorString(e));
+    return acc ? launch_column_sum(g.part, static_cast<int>(grid), K, dgamma, dbeta, stream) : QLIN_OK;
+  }
+  if (acc) {
     g.G = L.G;
     // before dX, which may replace dY or X
     cudaError_t e = launch_k(norm_columns_kernel, dim3((K / 8 + 127) / 128, L.G), dim3(128), 0, stream, g);
@@ -1739,8 +1807,7 @@ qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M,
   }
   if (!dX) return QLIN_OK;
   const dim3 grid(static_cast<unsigned>(M));
-  cudaError_t e = K <= 1024 ? launch_k(norm_rows_kernel<128>, grid, dim3(128), 0, stream, g)
-                            : launch_k(norm_rows_kernel<512>, grid, dim3(512), 0, stream, g);
+  cudaError_t e = launch_k(norm_rows_kernel<512>, grid, dim3(512), 0, stream, g);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "norm_rows_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
 }
