@@ -29,41 +29,83 @@ struct DactArgs {
   float* part;          // [G][N] partial column sums (columns kernel)
   float cmul;           // c'_n / c_n
   int M, N, act, G;
+  int stages;           // ring kernel
 };
 
-// dZ of the 8 channels of vector v of row m, in fp32.
+// dZ of 8 channels in fp32 from their packed values: z (8 halves) and dy (8,
+// gated: 4 in x and y).
 template <bool GATED>
-__device__ __forceinline__ void dact_vec(const DactArgs& g, size_t m, int v, float (&d)[8]) {
+__device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv, float (&d)[8]) {
   float z[8];
-  if (GATED || g.act != kActNone) h8_to_f(__ldg(reinterpret_cast<const uint4*>(g.Z + m * g.N) + v), z);
+  h8_to_f(zv, z);
   if (GATED) {
-    const uint2 h = __ldg(reinterpret_cast<const uint2*>(g.dY + m * (g.N >> 1)) + v);
-    const float2 a = __half22float2(u32_as_h2(h.x)), b = __half22float2(u32_as_h2(h.y));
+    const float2 a = __half22float2(u32_as_h2(yv.x)), b = __half22float2(u32_as_h2(yv.y));
     const float dy[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float val, slope;
-      act_slope(g.act, z[2 * i], val, slope);
+      act_slope(act, z[2 * i], val, slope);
       d[2 * i] = dy[i] * z[2 * i + 1] * slope;
       d[2 * i + 1] = dy[i] * val;
     }
   } else {
-    h8_to_f(__ldg(reinterpret_cast<const uint4*>(g.dY + m * g.N) + v), d);
-    if (g.act != kActNone) {
+    h8_to_f(yv, d);
+    if (act != kActNone) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float val, slope;
-        act_slope(g.act, z[i], val, slope);
+        act_slope(act, z[i], val, slope);
         d[i] *= slope;
       }
     }
   }
 }
 
+// A bound on |dZ| of those channels, up to the factor 1.13 of the slopes
+// (and |act(z)| <= |z|).
+template <bool GATED>
+__device__ __forceinline__ float dact_bound(const uint4 zv, const uint4 yv) {
+  if (GATED) {
+    float z[8];
+    h8_to_f(zv, z);
+    const float2 a = __half22float2(u32_as_h2(yv.x)), b = __half22float2(u32_as_h2(yv.y));
+    const float dy[4] = {a.x, a.y, b.x, b.y};
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(dy[i]) * fmaxf(fabsf(z[2 * i]), fabsf(z[2 * i + 1])));
+    return top;
+  }
+  const __half2 m = __hmax2(__hmax2(__habs2(u32_as_h2(yv.x)), __habs2(u32_as_h2(yv.y))),
+                            __hmax2(__habs2(u32_as_h2(yv.z)), __habs2(u32_as_h2(yv.w))));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+// 2^e with top 2^e in [2^13, 2^14), as its biased exponent: |dZ m_n| 2^e
+// stays below 2^14 * 1.13 * 2.3.  A row of zeros, or one that holds an
+// infinity, keeps e = 0.
+__device__ __forceinline__ uint32_t dact_exponent(float top) {
+  const uint32_t b = __float_as_uint(top) >> 23;
+  const uint32_t e = (b == 0u || b == 255u) ? 127u : 267u - b;
+  return e > 253u ? 253u : e;
+}
+
+// The packed values of vector v of row m from global memory.
+template <bool GATED>
+__device__ __forceinline__ void dact_load(const DactArgs& g, size_t m, int v, uint4& z, uint4& y) {
+  z = make_uint4(0u, 0u, 0u, 0u);
+  if (GATED || g.act != kActNone) z = __ldg(reinterpret_cast<const uint4*>(g.Z + m * g.N) + v);
+  if (GATED) {
+    const uint2 h = __ldg(reinterpret_cast<const uint2*>(g.dY + m * (g.N >> 1)) + v);
+    y = make_uint4(h.x, h.y, 0u, 0u);
+  } else {
+    y = __ldg(reinterpret_cast<const uint4*>(g.dY + m * g.N) + v);
+  }
+}
+
 constexpr int kDactThreads = 512;
 
-// One CTA per token row: the row's scale from a bound on |dZ| (slopes are
-// below 1.13, |act(z)| <= |z|), then dZ in one more pass over the row.
+// One CTA per token row: the row's scale from the bound, then dZ in one more
+// pass over the row.
 template <bool GATED>
 __global__ void __launch_bounds__(kDactThreads) dact_rows_kernel(const __grid_constant__ DactArgs g) {
   __shared__ float red[kDactThreads / 32];
@@ -73,21 +115,9 @@ __global__ void __launch_bounds__(kDactThreads) dact_rows_kernel(const __grid_co
   const int nv = g.N >> 3;
   float top = 0.f;
   for (int v = threadIdx.x; v < nv; v += kDactThreads) {
-    if (GATED) {
-      float z[8];
-      h8_to_f(__ldg(reinterpret_cast<const uint4*>(g.Z + m * g.N) + v), z);
-      const uint2 h = __ldg(reinterpret_cast<const uint2*>(g.dY + m * (g.N >> 1)) + v);
-      const float2 a = __half22float2(u32_as_h2(h.x)), b = __half22float2(u32_as_h2(h.y));
-      const float dy[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        top = fmaxf(top, fabsf(dy[i]) * fmaxf(fabsf(z[2 * i]), fabsf(z[2 * i + 1])));
-    } else {
-      float d[8];
-      h8_to_f(__ldg(reinterpret_cast<const uint4*>(g.dY + m * g.N) + v), d);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(d[i]));
-    }
+    uint4 z, y;
+    dact_load<GATED>(g, m, v, z, y);
+    top = fmaxf(top, dact_bound<GATED>(z, y));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -95,16 +125,14 @@ __global__ void __launch_bounds__(kDactThreads) dact_rows_kernel(const __grid_co
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kDactThreads / 32; ++w) top = fmaxf(top, red[w]);
-  // 2^e with top 2^e in [2^13, 2^14): |dZ m_n| 2^e stays below
-  // 2^14 * 1.13 * 2.  A row of zeros, or one that holds an infinity, keeps e = 0.
-  const uint32_t be = __float_as_uint(top) >> 23;
-  const uint32_t se = (be == 0u || be == 255u) ? 127u : 267u - be;  // biased exponent of 2^e
-  const uint32_t sc = se > 253u ? 253u : se;
-  const float scale = __uint_as_float(sc << 23);
-  if (threadIdx.x == 0) g.rowscale[m] = __uint_as_float((254u - sc) << 23);
+  const uint32_t e = dact_exponent(top);
+  const float scale = __uint_as_float(e << 23);
+  if (threadIdx.x == 0) g.rowscale[m] = __uint_as_float((254u - e) << 23);
   for (int v = threadIdx.x; v < nv; v += kDactThreads) {
+    uint4 z, y;
     float d[8], c[8];
-    dact_vec<GATED>(g, m, v, d);
+    dact_load<GATED>(g, m, v, z, y);
+    dact_vec<GATED>(g.act, z, y, d);
     load_f8(g.cscale + 8 * v, c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) d[i] = (d[i] * scale) * chan_mant(__fmul_rn(c[i], g.cmul));
@@ -123,14 +151,147 @@ __global__ void __launch_bounds__(128) dact_columns_kernel(const __grid_constant
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
   for (int m = blockIdx.y; m < g.M; m += g.G) {
+    uint4 z, y;
     float d[8];
-    dact_vec<GATED>(g, m, v, d);
+    dact_load<GATED>(g, m, v, z, y);
+    dact_vec<GATED>(g.act, z, y, d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] += d[i];
   }
   float4* p = reinterpret_cast<float4*>(g.part + static_cast<size_t>(blockIdx.y) * g.N) + 2 * v;
   p[0] = make_float4(s[0], s[1], s[2], s[3]);
   p[1] = make_float4(s[4], s[5], s[6], s[7]);
+}
+
+// Both at once over a row ring (norm.cuh): persistent CTAs of T threads, the
+// next rows on their way by bulk copies, thread t owning the vectors t,
+// t + T, ... (VPT at most).  One barrier a row, for the maximum of the bound;
+// the mantissas of the channel factors stay in registers where they fit
+// beside the column sums, which ACC keeps over the CTA's rows and writes once
+// as partial row blockIdx.x.  dZ is skipped when it is null (only the bias's
+// gradient is wanted).
+template <bool GATED, int T, int VPT, bool ACC>
+__global__ void __launch_bounds__(T) dact_ring_kernel(const __grid_constant__ DactArgs g) {
+  constexpr bool kKeep = VPT <= 4 || !ACC;
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ float red[2][32];
+  __shared__ uint64_t full[kRingStages];
+  __shared__ int abort_flag;
+  const int t = threadIdx.x;
+  const int nv = g.N >> 3;
+  const bool has_z = GATED || g.act != kActNone;
+  const uint32_t zb = has_z ? static_cast<uint32_t>(g.N) * 2u : 0u;
+  const uint32_t yb = static_cast<uint32_t>(g.N) * (GATED ? 1u : 2u);
+  const size_t stage = zb + yb;
+  const int S = g.stages;
+  if (t == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+  const size_t step = gridDim.x, M = static_cast<size_t>(g.M);
+  int issued = 0;  // rows on their way (thread 0)
+  auto load = [&](size_t m, int s) {
+    unsigned char* dst = ring_smem + s * stage;
+    mbar_arrive_expect_tx(&full[s], zb + yb);
+    if (has_z) bulk_load(dst, g.Z + m * g.N, zb, &full[s]);
+    bulk_load(dst + zb, g.dY + m * (GATED ? g.N >> 1 : g.N), yb, &full[s]);
+    ++issued;
+  };
+  if (t == 0)
+    for (int s = 0; s < S; ++s)
+      if (blockIdx.x + s * step < M) load(blockIdx.x + s * step, s);
+  float sum[ACC ? VPT : 1][8], mant[kKeep ? VPT : 1][8];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = t + j * T;
+    float c[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (kKeep && v < nv) load_f8(g.cscale + 8 * v, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (ACC) sum[j][e] = 0.f;
+      if (kKeep) mant[j][e] = chan_mant(__fmul_rn(c[e], g.cmul));
+    }
+  }
+  int i = 0;
+  for (size_t m = blockIdx.x; m < M; m += step, ++i) {
+    const int s = i % S;
+    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) abort_flag = 1;
+    const uint4* zr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
+    const unsigned char* yr = ring_smem + s * stage + zb;
+    auto values = [&](int v, uint4& z, uint4& y) {
+      z = has_z ? zr[v] : make_uint4(0u, 0u, 0u, 0u);
+      if (GATED) {
+        const uint2 h = reinterpret_cast<const uint2*>(yr)[v];
+        y = make_uint4(h.x, h.y, 0u, 0u);
+      } else {
+        y = reinterpret_cast<const uint4*>(yr)[v];
+      }
+    };
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (t + j * T < nv) {
+        uint4 z, y;
+        values(t + j * T, z, y);
+        top = fmaxf(top, dact_bound<GATED>(z, y));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((t & 31) == 0) red[i & 1][t >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) top = fmaxf(top, red[i & 1][w]);
+    if (t == 0 && i > 0 && abort_flag == 0) {  // the previous row's stage: every thread is done with it
+      const size_t next = m + static_cast<size_t>(S - 1) * step;
+      if (next < M) load(next, (i - 1) % S);
+    }
+    const uint32_t ex = dact_exponent(top);
+    const float scale = __uint_as_float(ex << 23);
+    if (t == 0 && g.dZ) g.rowscale[m] = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = t + j * T;
+      if (v < nv) {
+        uint4 z, y;
+        float d[8];
+        values(v, z, y);
+        dact_vec<GATED>(g.act, z, y, d);
+        if (ACC) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[j][e] += d[e];
+        }
+        if (g.dZ) {
+          if (kKeep) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = (d[e] * scale) * mant[j][e];
+          } else {
+            float c[8];
+            load_f8(g.cscale + 8 * v, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = (d[e] * scale) * chan_mant(__fmul_rn(c[e], g.cmul));
+          }
+          reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = f_to_h8(d);
+        }
+      }
+    }
+  }
+  if (t == 0 && abort_flag) drain_ring(full, S, issued);  // no copy outlives the CTA
+  if (ACC) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = t + j * T;
+      if (v < nv) {
+        float4* p = reinterpret_cast<float4*>(g.part + static_cast<size_t>(blockIdx.x) * g.N) + 2 * v;
+        p[0] = make_float4(sum[j][0], sum[j][1], sum[j][2], sum[j][3]);
+        p[1] = make_float4(sum[j][4], sum[j][5], sum[j][6], sum[j][7]);
+      }
+    }
+  }
 }
 
 }  // namespace qlin

@@ -61,11 +61,13 @@ struct DxWidenArgs {
 // of 64 channels x 128 inputs out: channel groups of 8 (2 KiB), in them two
 // atoms of 64 inputs (1 KiB), in them a 128-byte row per channel with the
 // tensor core's 128-byte swizzle (inputs contiguous: the packed rows'
-// direction, so nothing is transposed).  Eight neighbouring threads write one
-// row.
+// direction, so nothing is transposed).  The blocks are put together in
+// shared memory, eight threads a row, the outlier inputs are blended there
+// by two threads a row, and one bulk copy each takes them out.
 template <int FMT>
 __global__ void __launch_bounds__(256) dx_widen_kernel(const __grid_constant__ DxWidenArgs g) {
-  __shared__ __align__(16) int16_t orow[128];  // outlier entry of each input of the block, or -1
+  __shared__ __align__(128) unsigned char blk[32768];
+  __shared__ int first, count;  // the block's outliers: consecutive entries of the sorted list
   griddep_launch_dependents();
   const int tn = static_cast<int>(blockIdx.x) / g.kb;
   const int kb = static_cast<int>(blockIdx.x) - tn * g.kb;
@@ -90,28 +92,26 @@ __global__ void __launch_bounds__(256) dx_widen_kernel(const __grid_constant__ D
     c[i] = n < g.N ? bwd_chan<FMT>(__ldg(g.cscale + n)) : 0.f;
     rb[i] = (FMT == kFmtW4G128 && n < g.N) ? __ldg(g.rfold + static_cast<size_t>(kb) * g.N + n) : uint16_t(0);
   }
-  griddep_wait();  // s comes from the forward; the workspace may still be read
-  // which inputs of the block are outliers: the whole list read at once (a
-  // binary search is a chain of dependent loads: 10 us a block)
-  int nout = 0;
   if (g.nO > 0) {
-    if (threadIdx.x < 128) orow[threadIdx.x] = -1;
+    // which entries: the whole list read at once (a binary search is a chain
+    // of dependent loads)
+    if (threadIdx.x == 0) {
+      first = g.nO;
+      count = 0;
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < g.nO; i += 256) {
       const int k = __ldg(g.oidx + i) - kb * 128;
       if (k >= 0 && k < 128) {
-        orow[k] = static_cast<int16_t>(i);
-        nout = 1;
+        atomicMin(&first, i);
+        atomicAdd(&count, 1);
       }
     }
-    nout = __syncthreads_or(nout);
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int u = threadIdx.x + i * 256;
     const int row = u >> 4, cc = u & 15;
-    const int j = tn * 2 + (row >> 6);
-    if (j >= g.nst) break;  // rows ascend with i: the last channel tile may hold one block
     uint32_t q0, q1;
     if (FMT == kFmtW8) {
       q0 = w0[i];
@@ -130,26 +130,33 @@ __global__ void __launch_bounds__(256) dx_widen_kernel(const __grid_constant__ D
     uint4 h;
     i8x4_scale_h2(q0, p2, h.x, h.y);
     i8x4_scale_h2(q1, p2, h.z, h.w);
-    if (nout > 0) {
-      const uint4 ov = *reinterpret_cast<const uint4*>(orow + cc * 8);
-      if ((ov.x & ov.y & ov.z & ov.w) != 0xFFFFFFFFu) {
-        const float m = chan_mant(c[i]);
-        const float rm = m > 0.f ? __fdiv_rn(1.f, m) : 0.f;  // a channel without a scale has only zero weights
-        __half* e = reinterpret_cast<__half*>(&h);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const int o = orow[cc * 8 + t];
-          if (o >= 0) {
-            const float sv = g.s[o];
-            const float w = __half2float(__ushort_as_half(__ldg(g.wot + wot_tile_index(tn * 128 + row, o, g.nib))));
-            e[t] = __float2half_rn(__fdiv_rn(__fmaf_rn(__fsub_rn(sv, 1.f), __fmul_rn(w, rm), __half2float(e[t])), sv));
-          }
-        }
-      }
+    *reinterpret_cast<uint4*>(blk + (row >> 3) * 2048 + (cc >> 3) * 1024 + (row & 7) * 128 + (((cc & 7) ^ (row & 7)) << 4)) = h;
+  }
+  griddep_wait();  // s comes from the forward; the workspace may still be read
+  __syncthreads();
+  if (g.nO > 0 && count > 0) {
+    const int row = threadIdx.x >> 1;
+    const int n = tn * 128 + row;
+    const float m = n < g.N ? chan_mant(bwd_chan<FMT>(__ldg(g.cscale + n))) : 0.f;
+    const float rm = m > 0.f ? __fdiv_rn(1.f, m) : 0.f;  // a channel without a scale has only zero weights
+    for (int e = threadIdx.x & 1; e < count; e += 2) {
+      const int o = first + e;
+      const int k = __ldg(g.oidx + o) - kb * 128;
+      const float sv = g.s[o];
+      const float w = __half2float(__ushort_as_half(__ldg(g.wot + wot_tile_index(n, o, g.nib))));
+      __half* p = reinterpret_cast<__half*>(blk + (row >> 3) * 2048 + (k >> 6) * 1024 + (row & 7) * 128 +
+                                            ((((k & 63) >> 3) ^ (row & 7)) << 4)) + (k & 7);
+      *p = __float2half_rn(__fdiv_rn(__fmaf_rn(__fsub_rn(sv, 1.f), __fmul_rn(w, rm), __half2float(*p)), sv));
     }
-    uint8_t* dst = g.out + (static_cast<size_t>(kb) * g.nst + j) * 16384 + ((row & 63) >> 3) * 2048 + (cc >> 3) * 1024 +
-                   (row & 7) * 128 + (((cc & 7) ^ (row & 7)) << 4);
-    *reinterpret_cast<uint4*>(dst) = h;
+  }
+  fence_proxy_async_smem();  // the bulk copies read the blocks next
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b)
+      if (tn * 2 + b < g.nst)
+        bulk_store(g.out + (static_cast<size_t>(kb) * g.nst + tn * 2 + b) * 16384, blk + b * 16384, 16384u);
+    bulk_commit_group();
+    bulk_wait_group_all();
   }
 }
 

@@ -1166,6 +1166,58 @@ DxPlan plan_dx(int M, const qlin_weights* w) {
   return p;
 }
 
+// Rings of `rows` rows a stage: threads and vectors per thread of a row of K,
+// persistent CTAs per SM; ctas = 0 where the ring does not fit.
+struct RingPlan {
+  int threads, vpt, ctas, stages;
+  size_t smem;
+};
+RingPlan ring_plan(int K, int rows) {
+  RingPlan p{};
+  const int nv = K / 8;
+  p.threads = nv <= 128 ? 128 : (nv <= 256 ? 256 : 512);
+  p.vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);
+  p.stages = kRingStages;
+  p.smem = ring_bytes(K, rows);
+  const int fit = static_cast<int>(size_t(220) * 1024 / p.smem);
+  const int most = p.vpt == 4 ? 1 : (p.threads == 512 ? 2 : 4);
+  p.ctas = nv > 2048 ? 0 : (fit < most ? fit : most);
+  return p;
+}
+
+template <typename Args>
+cudaError_t launch_ring(void (*kern)(Args), const RingPlan& p, unsigned grid, cudaStream_t stream, const Args& g) {
+  // raising a kernel's shared-memory limit is idempotent and needs no stream
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.smem));
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(grid), dim3(p.threads), p.smem, stream, g);
+}
+
+unsigned ring_grid(const RingPlan& p, int M) {
+  const int most = sm_count() * p.ctas;
+  return static_cast<unsigned>(M < most ? M : most);
+}
+
+// The ring of the activation's backward pass: two or three stages of Z and
+// dY rows (ctas = 0 where two do not fit, or a thread would own more than
+// eight vectors).
+RingPlan dact_ring_plan(int N, bool gated, bool has_z) {
+  RingPlan p{};
+  const int nv = N / 8;
+  const size_t stage = size_t(N) * ((has_z ? 2 : 0) + (gated ? 1 : 2));
+  const size_t room = size_t(220) * 1024;
+  p.threads = nv <= 128 ? 128 : 512;
+  p.vpt = (nv + p.threads - 1) / p.threads;
+  p.vpt = p.vpt <= 4 ? p.vpt : (p.vpt <= 6 ? 6 : 8);
+  p.stages = static_cast<int>(room / stage < size_t(kRingStages) ? room / stage : kRingStages);
+  if (p.stages < 2 || nv > 8 * p.threads) return p;
+  p.smem = stage * p.stages;
+  const int fit = static_cast<int>(room / p.smem);
+  const int most = p.threads == 128 ? 8 : (p.vpt <= 2 ? 2 : 1);
+  p.ctas = fit < most ? fit : most;
+  return p;
+}
+
 // Workspace of a fused layer's backward pass: the widened weight operand, the
 // scaled dZ, the rows' factors, the partial sums of split tiles and of the
 // bias's gradient.
@@ -1182,10 +1234,30 @@ FusedBwdLayout fused_bwd_layout(int M, const qlin_weights* w) {
   L.dz = off; off = round_up(off + size_t(M) * w->N * 2, kAlign);
   L.rows = off; off = round_up(off + size_t(M) * 4, kAlign);
   L.dxpart = off; off = round_up(off + (L.dx.S > 1 ? size_t(L.dx.S) * M * w->K * 4 : 0), kAlign);
+  // partial rows of the bias's gradient: one per CTA of a ring kernel (whose
+  // shape depends on what it reads), else one per row group
   L.G = column_groups(M, w->N / 8);
-  L.part = off; off = round_up(off + size_t(L.G) * w->N * 4, kAlign);
+  int most = L.G;
+  for (int v = 0; v < 3; ++v) {
+    const int n = static_cast<int>(ring_grid(dact_ring_plan(w->N, v == 2, v >= 1), M));
+    if (n > most) most = n;
+  }
+  L.part = off; off = round_up(off + size_t(most) * w->N * 4, kAlign);
   L.total = off;
   return L;
+}
+
+template <bool GATED, bool ACC>
+cudaError_t launch_dact_ring(const RingPlan& p, unsigned grid, const DactArgs& g, cudaStream_t stream) {
+  if (p.threads == 128) return launch_ring(dact_ring_kernel<GATED, 128, 1, ACC>, p, grid, stream, g);
+  switch (p.vpt) {
+    case 1: return launch_ring(dact_ring_kernel<GATED, 512, 1, ACC>, p, grid, stream, g);
+    case 2: return launch_ring(dact_ring_kernel<GATED, 512, 2, ACC>, p, grid, stream, g);
+    case 3: return launch_ring(dact_ring_kernel<GATED, 512, 3, ACC>, p, grid, stream, g);
+    case 4: return launch_ring(dact_ring_kernel<GATED, 512, 4, ACC>, p, grid, stream, g);
+    case 6: return launch_ring(dact_ring_kernel<GATED, 512, 6, ACC>, p, grid, stream, g);
+    default: return launch_ring(dact_ring_kernel<GATED, 512, 8, ACC>, p, grid, stream, g);
+  }
 }
 
 template <int FMT>
@@ -1274,15 +1346,31 @@ qlin_status backward_fused(const qlin_weights* w, const uint16_t* dY, const uint
   g.N = w->N;
   g.act = act;
   g.G = L.G;
-  if (dbias) {
-    cudaError_t e = launch_k(dact_columns_kernel<GATED>, dim3((w->N / 8 + 127) / 128, L.G), dim3(128), 0, stream, g);
-    if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_columns_kernel launch failed: %s", cudaGetErrorString(e));
-    st = launch_column_sum(g.part, L.G, w->N, dbias, nullptr, stream);
-    if (st != QLIN_OK) return st;
+  const RingPlan ring = dact_ring_plan(w->N, GATED, needs_z);
+  cudaError_t e;
+  if (ring.ctas > 0) {
+    const unsigned grid = ring_grid(ring, M);
+    g.stages = ring.stages;
+    if (!dX) g.dZ = nullptr;
+    e = dbias ? launch_dact_ring<GATED, true>(ring, grid, g, stream) : launch_dact_ring<GATED, false>(ring, grid, g, stream);
+    if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_ring_kernel launch failed: %s", cudaGetErrorString(e));
+    if (dbias) {
+      st = launch_column_sum(g.part, static_cast<int>(grid), w->N, dbias, nullptr, stream);
+      if (st != QLIN_OK) return st;
+    }
+  } else {
+    if (dbias) {
+      e = launch_k(dact_columns_kernel<GATED>, dim3((w->N / 8 + 127) / 128, L.G), dim3(128), 0, stream, g);
+      if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_columns_kernel launch failed: %s", cudaGetErrorString(e));
+      st = launch_column_sum(g.part, L.G, w->N, dbias, nullptr, stream);
+      if (st != QLIN_OK) return st;
+    }
+    if (dX) {
+      e = launch_k(dact_rows_kernel<GATED>, dim3(static_cast<unsigned>(M)), dim3(kDactThreads), 0, stream, g);
+      if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_rows_kernel launch failed: %s", cudaGetErrorString(e));
+    }
   }
   if (!dX) return QLIN_OK;
-  cudaError_t e = launch_k(dact_rows_kernel<GATED>, dim3(static_cast<unsigned>(M)), dim3(kDactThreads), 0, stream, g);
-  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_rows_kernel launch failed: %s", cudaGetErrorString(e));
   DxWidenArgs a{};
   a.codes = static_cast<const uint8_t*>(w->codes);
   a.rfold = w->fold_ratio;
@@ -1315,37 +1403,6 @@ template <int T, int VPT>
 cudaError_t launch_norm_t(const NormFwdArgs& g, cudaStream_t stream) {
   const unsigned grid = T == 32 ? (static_cast<unsigned>(g.M) + 3) / 4 : static_cast<unsigned>(g.M);
   return launch_k(norm_forward_kernel<T, VPT>, dim3(grid), dim3(T == 32 ? 128 : T), 0, stream, g);
-}
-
-// Rings of `rows` rows a stage: threads and vectors per thread of a row of K,
-// persistent CTAs per SM; ctas = 0 where the ring does not fit.
-struct RingPlan {
-  int threads, vpt, ctas;
-  size_t smem;
-};
-RingPlan ring_plan(int K, int rows) {
-  RingPlan p{};
-  const int nv = K / 8;
-  p.threads = nv <= 128 ? 128 : (nv <= 256 ? 256 : 512);
-  p.vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);
-  p.smem = ring_bytes(K, rows);
-  const int fit = static_cast<int>(size_t(220) * 1024 / p.smem);
-  const int most = p.vpt == 4 ? 1 : (p.threads == 512 ? 2 : 4);
-  p.ctas = nv > 2048 ? 0 : (fit < most ? fit : most);
-  return p;
-}
-
-template <typename Args>
-cudaError_t launch_ring(void (*kern)(Args), const RingPlan& p, unsigned grid, cudaStream_t stream, const Args& g) {
-  // raising a kernel's shared-memory limit is idempotent and needs no stream
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.smem));
-  if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(grid), dim3(p.threads), p.smem, stream, g);
-}
-
-unsigned ring_grid(const RingPlan& p, int M) {
-  const int most = sm_count() * p.ctas;
-  return static_cast<unsigned>(M < most ? M : most);
 }
 
 template <bool ACC>

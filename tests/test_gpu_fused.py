@@ -272,6 +272,16 @@ def test_backward_every_activation(q, oracle, act, gated):
     check_backward(Layer(q, oracle, synth.W8_PERCHANNEL, 70, 256, 528, 12, gated=gated), act)
 
 
+@pytest.mark.parametrize("N", [1040, 4112, 8208, 12304, 16400, 24592, 32768, 32784, 40000])
+@pytest.mark.parametrize("gated", [False, True])
+def test_backward_wide_layers(q, oracle, gated, N):
+    """Every width class of the activation's backward pass, on both sides of
+    its edges and past the last."""
+    for M, with_dbias in ((3, True), (310, True), (5, False)):
+        check_backward(Layer(q, oracle, synth.W8_PERCHANNEL, M, 128, N, 2, gated=gated), "silu", with_dbias=with_dbias)
+    check_backward(Layer(q, oracle, synth.W8_PERCHANNEL, 4, 128, N, 2, gated=gated), "none")
+
+
 @pytest.mark.parametrize("dy_std", [3e-7, 2.0 ** -7, 3000.0])
 def test_backward_gradient_scales(q, oracle, dy_std):
     """The row's power of two keeps tiny and huge gradients in range: dH * up
