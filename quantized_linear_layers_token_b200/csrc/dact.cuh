@@ -41,22 +41,21 @@ __device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv
   if (GATED) {
     const float2 a = __half22float2(u32_as_h2(yv.x)), b = __half22float2(u32_as_h2(yv.y));
     const float dy[4] = {a.x, a.y, b.x, b.y};
+    const float gate[4] = {z[0], z[2], z[4], z[6]};
+    float val[4], slope[4];
+    act_slopes<4>(act, gate, val, slope);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float val, slope;
-      act_slope(act, z[2 * i], val, slope);
-      d[2 * i] = dy[i] * z[2 * i + 1] * slope;
-      d[2 * i + 1] = dy[i] * val;
+      d[2 * i] = dy[i] * z[2 * i + 1] * slope[i];
+      d[2 * i + 1] = dy[i] * val[i];
     }
   } else {
     h8_to_f(yv, d);
     if (act != kActNone) {
+      float val[8], slope[8];
+      act_slopes<8>(act, z, val, slope);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float val, slope;
-        act_slope(act, z[i], val, slope);
-        d[i] *= slope;
-      }
+      for (int i = 0; i < 8; ++i) d[i] *= slope[i];
     }
   }
 }
@@ -163,21 +162,21 @@ __global__ void __launch_bounds__(128) dact_columns_kernel(const __grid_constant
   p[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
-// Both at once over a row ring (norm.cuh): persistent CTAs of T threads, the
-// next rows on their way by bulk copies, thread t owning the vectors t,
-// t + T, ... (VPT at most).  One barrier a row, for the maximum of the bound;
+// Both at once over a row ring (norm.cuh, one row a stage): persistent CTAs of
+// T threads, the next rows on their way by bulk copies, thread t owning the
+// vectors t, t + T, ... (VPT at most).  One barrier a row, for the maximum of the bound;
 // the mantissas of the channel factors stay in registers where they fit
 // beside the column sums, which ACC keeps over the CTA's rows and writes once
 // as partial row blockIdx.x.  dZ is skipped when it is null (only the bias's
 // gradient is wanted).
-template <bool GATED, int T, int VPT, bool ACC>
-__global__ void __launch_bounds__(T) dact_ring_kernel(const __grid_constant__ DactArgs g) {
-  constexpr bool kKeep = VPT <= 4 || !ACC;
+template <bool GATED, int VPT, bool ACC>
+__global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__ DactArgs g) {
+  constexpr bool kKeep = VPT * (ACC ? 2 : 1) <= 3;
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ float red[2][32];
   __shared__ uint64_t full[kRingStages];
   __shared__ int abort_flag;
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, T = static_cast<int>(blockDim.x), nw = T >> 5;
   const int nv = g.N >> 3;
   const bool has_z = GATED || g.act != kActNone;
   const uint32_t zb = has_z ? static_cast<uint32_t>(g.N) * 2u : 0u;
@@ -244,8 +243,9 @@ __global__ void __launch_bounds__(T) dact_ring_kernel(const __grid_constant__ Da
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if ((t & 31) == 0) red[i & 1][t >> 5] = top;
     __syncthreads();
+    top = (t & 31) < nw ? red[i & 1][t & 31] : 0.f;
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) top = fmaxf(top, red[i & 1][w]);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (t == 0 && i > 0 && abort_flag == 0) {  // the previous row's stage: every thread is done with it
       const size_t next = m + static_cast<size_t>(S - 1) * step;
       if (next < M) load(next, (i - 1) % S);

@@ -63,35 +63,48 @@ __device__ __forceinline__ void act_values(int act, float (&z)[N]) {
   }
 }
 
-// act(z) and act'(z).
-__device__ __forceinline__ void act_slope(int act, float z, float& value, float& slope) {
+// act(z) and act'(z) of N values.
+template <int N>
+__device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (&value)[N], float (&slope)[N]) {
   switch (act) {
     case kActRelu:
-      value = z < 0.f ? 0.f : z;
-      slope = z > 0.f ? 1.f : 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        value[i] = z[i] < 0.f ? 0.f : z[i];
+        slope[i] = z[i] > 0.f ? 1.f : 0.f;
+      }
       break;
-    case kActGelu: {
-      const float p = normcdff(z);
-      value = z * p;
-      slope = fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), p);
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float p = normcdff(z[i]);
+        value[i] = z[i] * p;
+        slope[i] = fmaf(z[i] * 0.3989422804014327f, __expf(-0.5f * z[i] * z[i]), p);
+      }
       break;
-    }
-    case kActGeluTanh: {
-      const float z2 = z * z;
-      const float p = sigmoid_f(kGeluTanhA * fmaf(kGeluTanhB * z, z2, z));
-      value = z * p;
-      slope = fmaf(z * p * (1.f - p), kGeluTanhA * fmaf(3.f * kGeluTanhB, z2, 1.f), p);
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float z2 = z[i] * z[i];
+        const float p = sigmoid_f(kGeluTanhA * fmaf(kGeluTanhB * z[i], z2, z[i]));
+        value[i] = z[i] * p;
+        slope[i] = fmaf(z[i] * p * (1.f - p), kGeluTanhA * fmaf(3.f * kGeluTanhB, z2, 1.f), p);
+      }
       break;
-    }
-    case kActSilu: {
-      const float p = sigmoid_f(z);
-      value = z * p;
-      slope = p * fmaf(z, 1.f - p, 1.f);
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float p = sigmoid_f(z[i]);
+        value[i] = z[i] * p;
+        slope[i] = p * fmaf(z[i], 1.f - p, 1.f);
+      }
       break;
-    }
     default:
-      value = z;
-      slope = 1.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        value[i] = z[i];
+        slope[i] = 1.f;
+      }
   }
 }
 

@@ -71,6 +71,38 @@ __device__ __forceinline__ void load_f8(const float* p, float (&f)[8]) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
+// The same eight values as four fp32 pairs.
+__device__ __forceinline__ void h8_to_f2(const uint4 v, f32x2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+    f[e] = f2_pack(t.x, t.y);
+  }
+}
+__device__ __forceinline__ uint4 f2_to_h8(const f32x2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 t = f2_unpack(f[e]);
+    const __half2 h = __floats2half2_rn(t.x, t.y);
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void load_f2x4(const float* p, f32x2 (&f)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = f2_pack(a.x, a.y);
+  f[1] = f2_pack(a.z, a.w);
+  f[2] = f2_pack(b.x, b.y);
+  f[3] = f2_pack(b.z, b.w);
+}
+__device__ __forceinline__ float f2_sum(f32x2 v) {
+  const float2 t = f2_unpack(v);
+  return t.x + t.y;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -133,7 +165,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T) norm_forward_kernel(const _
       for (int e = 0; e < 8; ++e) q = fmaf(f[e] - mu, f[e] - mu, q);
     }
   }
-  const float r = 1.f / sqrtf(fmaf(row_sum<T>(q, red[1]), invk, g.eps));
+  const float r = rsqrtf(fmaf(row_sum<T>(q, red[1]), invk, g.eps));
   uint4* yr = reinterpret_cast<uint4*>(g.Y + static_cast<size_t>(m) * g.K);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -208,36 +240,85 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
   if (c == 0 && static_cast<int>(blockIdx.x) * 32 + w < K) out[blockIdx.x * 32 + w] = s;
 }
 
-// ---- Row rings: persistent CTAs of T threads work through the rows
-// blockIdx.x, + gridDim.x, ...; one thread keeps the next kRingStages rows on
-// their way into shared memory with bulk copies, so the loads do not wait for
-// the row in hand and need no registers.  Thread t owns the 8-element
-// vectors t, t + T, ... of every row, VPT of them at most.
+// ---- Row rings: persistent CTAs work through groups of R neighbouring rows,
+// blockIdx.x, + gridDim.x, ...; one thread keeps the next groups on their way
+// into shared memory with bulk copies, so the loads do not wait for the rows
+// in hand and need no registers.  Thread t owns the 8-element vectors t,
+// t + T, ... of every row, VPT of them at most (T threads a CTA).  A row
+// costs its element work and a share of a barrier: R rows reduce together,
+// which is what a row at a time spent most of its time on.
 constexpr int kRingStages = 3;
 
-// The next row of a stage: `n` arrays of `bytes` each, one after the other.
+// Sums of NV values over the CTA's `nw` warps, returned to every thread.  In
+// the warp, lanes exchange halves of the values (recursive halving), so NV
+// values cost about NV + 3 shuffles instead of 5 NV; the warps' sums meet in
+// `red` ([NV][32], one of two alternating buffers: one barrier a call).
+template <int NV>
+__device__ __forceinline__ void cta_sums(float (&v)[NV], float (*red)[32], int nw) {
+  static_assert(NV == 1 || NV == 2 || NV == 4 || NV == 8, "a power of two up to 8");
+  const int lane = threadIdx.x & 31;
+  float x[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = v[i];
+  // after the step of lane bit b, lanes with the bit set keep the upper half
+#pragma unroll
+  for (int n = NV / 2, b = 16; n >= 1; n >>= 1, b >>= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? x[i] : x[n + i];
+      const float keep = up ? x[n + i] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, b);
+    }
+  }
+#pragma unroll
+  for (int b = 16 / NV; b >= 1; b >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], b);
+  // lane bits 16, 8, 4 (as many as halvings) name the value held
+  constexpr int kSpan = 32 / NV;  // lanes that hold the same value
+  const int mine = lane / kSpan;
+  if (nw > 1) {
+    if (lane % kSpan == 0) red[mine][threadIdx.x >> 5] = x[0];
+    __syncthreads();
+    x[0] = 0.f;
+    for (int w = lane % kSpan; w < nw; w += kSpan) x[0] += red[mine][w];
+#pragma unroll
+    for (int b = kSpan / 2; b >= 1; b >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], b);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, x[0], i * kSpan);
+}
+
+// A group of rows [row, row + n) of the arrays a, b, c (the last two may be
+// null), one array after the other in the stage, R rows apart.
 __device__ __forceinline__ void ring_load(unsigned char* dst, const uint16_t* a, const uint16_t* b, const uint16_t* c,
-                                          size_t row, int K, uint64_t* bar) {
-  const uint32_t bytes = static_cast<uint32_t>(K) * 2u;
+                                          size_t row, int n, int R, int K, uint64_t* bar) {
+  const uint32_t bytes = static_cast<uint32_t>(n) * static_cast<uint32_t>(K) * 2u;
+  const size_t next = static_cast<size_t>(R) * K * 2;
   mbar_arrive_expect_tx(bar, bytes * (1u + (b ? 1u : 0u) + (c ? 1u : 0u)));
   bulk_load(dst, a + row * K, bytes, bar);
-  if (b) bulk_load(dst + bytes, b + row * K, bytes, bar);
-  if (c) bulk_load(dst + 2 * bytes, c + row * K, bytes, bar);
+  if (b) bulk_load(dst + next, b + row * K, bytes, bar);
+  if (c) bulk_load(dst + 2 * next, c + row * K, bytes, bar);
 }
 
 // Shared memory of a ring: the stages of `rows` rows of K values.
 __host__ __device__ inline size_t ring_bytes(int K, int rows) { return size_t(kRingStages) * rows * K * 2; }
 
-// Forward over a ring.  gamma and beta stay in registers (VPT <= 2).
-template <int T, int VPT>
-__global__ void __launch_bounds__(T) norm_forward_ring_kernel(const __grid_constant__ NormFwdArgs g) {
+__device__ __forceinline__ int group_rows(size_t grp, int R, int M) {  // rows of group grp that exist
+  const size_t left = static_cast<size_t>(M) - grp * R;
+  return left < static_cast<size_t>(R) ? static_cast<int>(left) : R;
+}
+
+// Forward over a ring.  gamma and beta stay in registers.
+template <int VPT, int R>
+__global__ void __launch_bounds__(512) norm_forward_ring_kernel(const __grid_constant__ NormFwdArgs g) {
   extern __shared__ __align__(128) unsigned char ring_smem[];
-  __shared__ float red[2][2][32];
+  __shared__ float red[4][R][32];
   __shared__ uint64_t full[kRingStages];
   __shared__ int abort_flag;
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, T = static_cast<int>(blockDim.x), nw = T >> 5;
   const int nv = g.K >> 3;
-  const size_t stage = static_cast<size_t>(g.K) * 2;
+  const size_t stage = static_cast<size_t>(R) * g.K * 2;
+  const size_t groups = (static_cast<size_t>(g.M) + R - 1) / R, step = gridDim.x;
   if (t == 0) {
     for (int s = 0; s < kRingStages; ++s) mbar_init(&full[s], 1);
     abort_flag = 0;
@@ -246,79 +327,93 @@ __global__ void __launch_bounds__(T) norm_forward_ring_kernel(const __grid_const
   __syncthreads();
   griddep_launch_dependents();
   griddep_wait();
-  const int step = static_cast<int>(gridDim.x);
-  int issued = 0;  // rows on their way (thread 0)
-  if (t == 0) {
-    for (int s = 0; s < kRingStages; ++s) {
-      const size_t m = blockIdx.x + static_cast<size_t>(s) * step;
-      if (m < static_cast<size_t>(g.M)) {
-        ring_load(ring_smem + s * stage, g.X, nullptr, nullptr, m, g.K, &full[s]);
-        ++issued;
-      }
-    }
-  }
-  float gm[VPT][8], bt[VPT][8];
+  int issued = 0;  // groups on their way (thread 0)
+  auto load = [&](size_t grp, int s) {
+    ring_load(ring_smem + s * stage, g.X, nullptr, nullptr, grp * R, group_rows(grp, R, g.M), R, g.K, &full[s]);
+    ++issued;
+  };
+  if (t == 0)
+    for (int s = 0; s < kRingStages; ++s)
+      if (blockIdx.x + s * step < groups) load(blockIdx.x + s * step, s);
+  f32x2 gm[VPT][4], bt[VPT][4];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = t + j * T;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gm[j][e] = bt[j][e] = 0.f;
+    for (int e = 0; e < 4; ++e) gm[j][e] = bt[j][e] = f2_both(0.f);
     if (v < nv) {
-      load_f8(g.gamma + 8 * v, gm[j]);
-      if (g.beta) load_f8(g.beta + 8 * v, bt[j]);
+      load_f2x4(g.gamma + 8 * v, gm[j]);
+      if (g.beta) load_f2x4(g.beta + 8 * v, bt[j]);
     }
   }
   const float invk = 1.f / static_cast<float>(g.K);
   int i = 0;
-  for (size_t m = blockIdx.x; m < static_cast<size_t>(g.M); m += step, ++i) {
+  for (size_t grp = blockIdx.x; grp < groups; grp += step, ++i) {
     const int s = i % kRingStages;
+    const int rows = group_rows(grp, R, g.M);
+    const size_t m0 = grp * R;
     if (!mbar_wait(&full[s], static_cast<uint32_t>(i / kRingStages) & 1u, &abort_flag)) abort_flag = 1;
     const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
-    uint4 x[VPT];
+    f32x2 x[R][VPT][4];  // the rows' values, then x - mu
+    float mu[R], q[R];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) x[j] = t + j * T < nv ? xr[t + j * T] : make_uint4(0u, 0u, 0u, 0u);
-    float mu = 0.f;
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        h8_to_f2(t + j * T < nv ? xr[r * nv + t + j * T] : make_uint4(0u, 0u, 0u, 0u), x[r][j]);
+      mu[r] = 0.f;
+    }
     if (!g.rms) {
-      float a = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        f32x2 a = x[r][0][0];
+#pragma unroll
+        for (int k = 1; k < 4 * VPT; ++k) a = f2_add(a, x[r][k >> 2][k & 3]);
+        mu[r] = f2_sum(a);
+      }
+      cta_sums<R>(mu, red[2 * (i & 1)], nw);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        mu[r] *= invk;
+        const f32x2 nmu = f2_both(-mu[r]);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+          if (t + j * T < nv)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[r][j][e] = f2_add(x[r][j][e], nmu);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      f32x2 a = f2_mul(x[r][0][0], x[r][0][0]);
+#pragma unroll
+      for (int k = 1; k < 4 * VPT; ++k) a = f2_fma(x[r][k >> 2][k & 3], x[r][k >> 2][k & 3], a);
+      q[r] = f2_sum(a);
+    }
+    cta_sums<R>(q, red[2 * (i & 1) + 1], nw);
+    if (nw == 1) __syncwarp();
+    // every thread holds its part of the rows (the sums' barrier): refill
+    if (t == 0) {
+      const size_t next = grp + static_cast<size_t>(kRingStages) * step;
+      if (abort_flag == 0 && next < groups) load(next, s);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= rows) break;
+      const float rs = rsqrtf(fmaf(q[r], invk, g.eps));
+      const f32x2 r2 = f2_both(rs);
+      uint4* yr = reinterpret_cast<uint4*>(g.Y + (m0 + r) * g.K);
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        float f[8];
-        h8_to_f(x[j], f);
+        if (t + j * T < nv) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a += f[e];
+          for (int e = 0; e < 4; ++e) x[r][j][e] = f2_fma(f2_mul(x[r][j][e], r2), gm[j][e], bt[j][e]);
+          yr[t + j * T] = f2_to_h8(x[r][j]);
+        }
       }
-      mu = row_sum<T>(a, red[i & 1][0]) * invk;
-    }
-    float q = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (t + j * T < nv) {
-        float f[8];
-        h8_to_f(x[j], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(f[e] - mu, f[e] - mu, q);
-      }
-    }
-    const float r = 1.f / sqrtf(fmaf(row_sum<T>(q, red[i & 1][1]), invk, g.eps));
-    // every thread holds its part of the row (the sum's barrier): refill
-    if (t == 0) {
-      const size_t next = m + static_cast<size_t>(kRingStages) * step;
-      if (abort_flag == 0 && next < static_cast<size_t>(g.M)) {
-        ring_load(ring_smem + s * stage, g.X, nullptr, nullptr, next, g.K, &full[s]);
-        ++issued;
-      }
-      if (g.mean) g.mean[m] = mu;
-      if (g.rstd) g.rstd[m] = r;
-    }
-    uint4* yr = reinterpret_cast<uint4*>(g.Y + m * g.K);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (t + j * T < nv) {
-        float f[8];
-        h8_to_f(x[j], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mu) * r, gm[j][e], bt[j][e]);
-        yr[t + j * T] = f_to_h8(f);
+      if (t == 0) {
+        if (g.mean) g.mean[m0 + r] = mu[r];
+        if (g.rstd) g.rstd[m0 + r] = rs;
       }
     }
   }
@@ -326,19 +421,23 @@ __global__ void __launch_bounds__(T) norm_forward_ring_kernel(const __grid_const
 }
 
 // Backward over a ring: dX, and with ACC the column sums of dy xh and dy over
-// the CTA's rows in registers, written once as partial row blockIdx.x.  Each
-// row costs one barrier: its two sums are taken together.  A stage is
-// refilled after the next row's barrier, when every thread is done with it.
-template <int T, int VPT, bool ACC>
-__global__ void __launch_bounds__(T) norm_backward_ring_kernel(const __grid_constant__ NormBwdArgs g) {
+// the CTA's rows in registers, written once as partial row blockIdx.x.  The
+// two sums of R rows are taken together: one barrier a group.  A stage is
+// refilled after the next group's barrier, when every thread is done with
+// it; xh and dy gamma are formed again from shared memory rather than kept.
+// gamma stays in registers where it fits (VPT <= 2).
+template <int VPT, int R, bool ACC>
+__global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_constant__ NormBwdArgs g) {
+  constexpr bool kGamma = VPT <= 2;
   extern __shared__ __align__(128) unsigned char ring_smem[];
-  __shared__ float red[2][2][32];
+  __shared__ float red[2][2 * R][32];
   __shared__ uint64_t full[kRingStages];
   __shared__ int abort_flag;
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, T = static_cast<int>(blockDim.x), nw = T >> 5;
   const int nv = g.K >> 3;
-  const size_t row_bytes = static_cast<size_t>(g.K) * 2;
-  const size_t stage = row_bytes * (g.dres ? 3 : 2);
+  const size_t part = static_cast<size_t>(R) * g.K * 2;
+  const size_t stage = part * (g.dres ? 3 : 2);
+  const size_t groups = (static_cast<size_t>(g.M) + R - 1) / R, step = gridDim.x;
   if (t == 0) {
     for (int s = 0; s < kRingStages; ++s) mbar_init(&full[s], 1);
     abort_flag = 0;
@@ -347,101 +446,100 @@ __global__ void __launch_bounds__(T) norm_backward_ring_kernel(const __grid_cons
   __syncthreads();
   griddep_launch_dependents();
   griddep_wait();
-  const size_t step = gridDim.x, M = static_cast<size_t>(g.M);
-  int issued = 0;  // rows on their way (thread 0)
-  if (t == 0) {
-    for (int s = 0; s < kRingStages; ++s) {
-      const size_t m = blockIdx.x + s * step;
-      if (m < M) {
-        ring_load(ring_smem + s * stage, g.dY, g.X, g.dres, m, g.K, &full[s]);
-        ++issued;
-      }
-    }
-  }
-  float sg[VPT][8], sb[VPT][8];
+  int issued = 0;  // groups on their way (thread 0)
+  auto load = [&](size_t grp, int s) {
+    ring_load(ring_smem + s * stage, g.dY, g.X, g.dres, grp * R, group_rows(grp, R, g.M), R, g.K, &full[s]);
+    ++issued;
+  };
+  if (t == 0)
+    for (int s = 0; s < kRingStages; ++s)
+      if (blockIdx.x + s * step < groups) load(blockIdx.x + s * step, s);
+  f32x2 sg[VPT][4], sb[VPT][4], gk[kGamma ? VPT : 1][4];
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sg[j][e] = sb[j][e] = 0.f;
-  const float invk = 1.f / static_cast<float>(g.K);
-  float mu1 = 0.f, r1 = 0.f;  // the next row's statistics, loaded a row ahead
-  if (blockIdx.x < M) {
-    if (!g.rms) mu1 = g.mean[blockIdx.x];
-    r1 = g.rstd[blockIdx.x];
+    for (int e = 0; e < 4; ++e) sg[j][e] = sb[j][e] = f2_both(0.f);
+  if (kGamma) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) gk[kGamma ? j : 0][e] = f2_both(0.f);
+      if (t + j * T < nv) load_f2x4(g.gamma + 8 * (t + j * T), gk[kGamma ? j : 0]);
+    }
   }
+  const float invk = 1.f / static_cast<float>(g.K);
   int i = 0;
-  for (size_t m = blockIdx.x; m < M; m += step, ++i) {
+  for (size_t grp = blockIdx.x; grp < groups; grp += step, ++i) {
     const int s = i % kRingStages;
-    const float mu = mu1, r = r1;
-    if (m + step < M) {
-      if (!g.rms) mu1 = g.mean[m + step];
-      r1 = g.rstd[m + step];
+    const int rows = group_rows(grp, R, g.M);
+    const size_t m0 = grp * R;
+    float mu[R], rs[R];  // read before the wait, so their latency passes with the rows'
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mu[r] = g.rms || r >= rows ? 0.f : g.mean[m0 + r];
+      rs[r] = r < rows ? g.rstd[m0 + r] : 0.f;
     }
     if (!mbar_wait(&full[s], static_cast<uint32_t>(i / kRingStages) & 1u, &abort_flag)) abort_flag = 1;
     const uint4* dr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
-    const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage + row_bytes);
-    const uint4* rr = reinterpret_cast<const uint4*>(ring_smem + s * stage + 2 * row_bytes);
-    float s1 = 0.f, s2 = 0.f;
+    const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage + part);
+    const uint4* rr = reinterpret_cast<const uint4*>(ring_smem + s * stage + 2 * part);
+    float sum[2 * R];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = t + j * T;
-      if (v < nv) {
-        float x[8], dy[8], gm[8];
-        h8_to_f(xr[v], x);
-        h8_to_f(dr[v], dy);
-        load_f8(g.gamma + 8 * v, gm);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xh = (x[e] - mu) * r;
-          if (ACC) {
-            sg[j][e] = fmaf(dy[e], xh, sg[j][e]);
-            sb[j][e] += dy[e];
-          }
-          const float w = dy[e] * gm[e];
-          s1 += w;
-          s2 = fmaf(w, xh, s2);
-        }
-      }
-    }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if ((t & 31) == 0) {
-      red[i & 1][0][t >> 5] = s1;
-      red[i & 1][1][t >> 5] = s2;
-    }
-    __syncthreads();
-    s1 = s2 = 0.f;
-#pragma unroll
-    for (int w = 0; w < T / 32; ++w) {
-      s1 += red[i & 1][0][w];
-      s2 += red[i & 1][1][w];
-    }
-    s1 = g.rms ? 0.f : s1 * invk;
-    s2 *= invk;
-    if (t == 0 && i > 0 && abort_flag == 0) {  // the previous row's stage
-      const size_t next = m + static_cast<size_t>(kRingStages - 1) * step;
-      const int p = (i - 1) % kRingStages;
-      if (next < M) {
-        ring_load(ring_smem + p * stage, g.dY, g.X, g.dres, next, g.K, &full[p]);
-        ++issued;
-      }
-    }
-    if (g.dX) {
+    for (int r = 0; r < R; ++r) {
+      f32x2 a1 = f2_both(0.f), a2 = f2_both(0.f);
+      const f32x2 nmu = f2_both(-mu[r]), r2 = f2_both(rs[r]);
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         const int v = t + j * T;
-        if (v < nv) {
-          float x[8], dy[8], gm[8], rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          h8_to_f(xr[v], x);
-          h8_to_f(dr[v], dy);
-          load_f8(g.gamma + 8 * v, gm);
-          if (g.dres) h8_to_f(rr[v], rs);
+        if (v < nv && r < rows) {
+          f32x2 xh[4], dy[4], gm[4];
+          h8_to_f2(xr[r * nv + v], xh);
+          h8_to_f2(dr[r * nv + v], dy);
+          if (!kGamma) load_f2x4(g.gamma + 8 * v, gm);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float xh = (x[e] - mu) * r;
-            x[e] = fmaf(r, dy[e] * gm[e] - s1 - xh * s2, rs[e]);
+          for (int e = 0; e < 4; ++e) {
+            xh[e] = f2_mul(f2_add(xh[e], nmu), r2);
+            if (ACC) {
+              sg[j][e] = f2_fma(dy[e], xh[e], sg[j][e]);
+              sb[j][e] = f2_add(sb[j][e], dy[e]);
+            }
+            const f32x2 w = f2_mul(dy[e], kGamma ? gk[kGamma ? j : 0][e] : gm[e]);
+            a1 = f2_add(a1, w);
+            a2 = f2_fma(w, xh[e], a2);
           }
-          reinterpret_cast<uint4*>(g.dX + m * g.K)[v] = f_to_h8(x);
+        }
+      }
+      sum[2 * r] = f2_sum(a1);
+      sum[2 * r + 1] = f2_sum(a2);
+    }
+    cta_sums<2 * R>(sum, red[i & 1], nw);
+    if (nw == 1) __syncwarp();
+    if (t == 0 && i > 0 && abort_flag == 0) {  // the previous group's stage
+      const size_t next = grp + static_cast<size_t>(kRingStages - 1) * step;
+      if (next < groups) load(next, (i - 1) % kRingStages);
+    }
+    if (g.dX) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        const f32x2 nmu = f2_both(-mu[r]), r2 = f2_both(rs[r]);
+        const f32x2 n1 = f2_both(g.rms ? 0.f : -sum[2 * r] * invk), n2 = f2_both(-sum[2 * r + 1] * invk);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          const int v = t + j * T;
+          if (v < nv) {
+            f32x2 x[4], dy[4], gm[4], res[4];
+            h8_to_f2(xr[r * nv + v], x);
+            h8_to_f2(dr[r * nv + v], dy);
+            if (!kGamma) load_f2x4(g.gamma + 8 * v, gm);
+            h8_to_f2(g.dres ? rr[r * nv + v] : make_uint4(0u, 0u, 0u, 0u), res);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const f32x2 xh = f2_mul(f2_add(x[e], nmu), r2);
+              x[e] = f2_fma(f2_fma(xh, n2, f2_add(f2_mul(dy[e], kGamma ? gk[kGamma ? j : 0][e] : gm[e]), n1)), r2, res[e]);
+            }
+            reinterpret_cast<uint4*>(g.dX + (m0 + r) * g.K)[v] = f2_to_h8(x);
+          }
         }
       }
     }
@@ -454,10 +552,13 @@ __global__ void __launch_bounds__(T) norm_backward_ring_kernel(const __grid_cons
       if (v < nv) {
         float4* pg = reinterpret_cast<float4*>(g.part + static_cast<size_t>(blockIdx.x) * g.K) + 2 * v;
         float4* pb = reinterpret_cast<float4*>(g.part + (step + blockIdx.x) * g.K) + 2 * v;
-        pg[0] = make_float4(sg[j][0], sg[j][1], sg[j][2], sg[j][3]);
-        pg[1] = make_float4(sg[j][4], sg[j][5], sg[j][6], sg[j][7]);
-        pb[0] = make_float4(sb[j][0], sb[j][1], sb[j][2], sb[j][3]);
-        pb[1] = make_float4(sb[j][4], sb[j][5], sb[j][6], sb[j][7]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 a = f2_unpack(sg[j][2 * e]), b = f2_unpack(sg[j][2 * e + 1]);
+          const float2 c = f2_unpack(sb[j][2 * e]), d = f2_unpack(sb[j][2 * e + 1]);
+          pg[e] = make_float4(a.x, a.y, b.x, b.y);
+          pb[e] = make_float4(c.x, c.y, d.x, d.y);
+        }
       }
     }
   }

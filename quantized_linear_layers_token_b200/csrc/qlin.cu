@@ -1166,22 +1166,41 @@ DxPlan plan_dx(int M, const qlin_weights* w) {
   return p;
 }
 
-// Rings of `rows` rows a stage: threads and vectors per thread of a row of K,
-// persistent CTAs per SM; ctas = 0 where the ring does not fit.
+// A row ring's shape: threads, vectors per thread, rows per group, stages and
+// persistent CTAs per SM (0 where the ring does not fit).
 struct RingPlan {
-  int threads, vpt, ctas, stages;
+  int threads, vpt, rows, ctas, stages;
   size_t smem;
 };
-RingPlan ring_plan(int K, int rows) {
+
+// Threads that own `vpt` of nv vectors each, in whole warps.
+int ring_threads(int nv, int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; }
+
+int ring_ctas(const RingPlan& p, int threads_per_sm) {
+  const int fit = static_cast<int>(size_t(220) * 1024 / p.smem);
+  int most = threads_per_sm / p.threads;
+  if (most > 16) most = 16;  // more would only lengthen the sums over the CTAs
+  return fit < most ? fit : most;
+}
+
+// Norms over `arrays` arrays of M rows.  A thread has about 32 values of a
+// row in hand (backward: 16 of two rows, whose column sums it keeps): with
+// fewer, what a row costs beside its values -- waits, reductions, addresses --
+// outweighs them.  Short rows are taken four or two at a time.
+RingPlan norm_ring_plan(int M, int K, int arrays, bool backward) {
   RingPlan p{};
   const int nv = K / 8;
-  p.threads = nv <= 128 ? 128 : (nv <= 256 ? 256 : 512);
-  p.vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);
+  if (nv > 2048) return p;
+  p.vpt = nv <= 32 ? 1 : (nv <= 64 || (backward && nv <= 1024) ? 2 : 4);
+  p.rows = 4 / p.vpt;
+  p.threads = ring_threads(nv, p.vpt);
   p.stages = kRingStages;
-  p.smem = ring_bytes(K, rows);
-  const int fit = static_cast<int>(size_t(220) * 1024 / p.smem);
-  const int most = p.vpt == 4 ? 1 : (p.threads == 512 ? 2 : 4);
-  p.ctas = nv > 2048 ? 0 : (fit < most ? fit : most);
+  for (;; p.rows = 1) {
+    p.smem = ring_bytes(K, p.rows * arrays);
+    p.ctas = ring_ctas(p, 512);
+    // one row at a time where groups would leave SMs idle or do not fit
+    if (p.rows == 1 || (p.ctas > 0 && (M + p.rows - 1) / p.rows >= sm_count())) break;
+  }
   return p;
 }
 
@@ -1194,27 +1213,26 @@ cudaError_t launch_ring(void (*kern)(Args), const RingPlan& p, unsigned grid, cu
 }
 
 unsigned ring_grid(const RingPlan& p, int M) {
-  const int most = sm_count() * p.ctas;
-  return static_cast<unsigned>(M < most ? M : most);
+  if (p.ctas == 0) return 0;
+  const int groups = (M + p.rows - 1) / p.rows, most = sm_count() * p.ctas;
+  return static_cast<unsigned>(groups < most ? groups : most);
 }
 
 // The ring of the activation's backward pass: two or three stages of Z and
 // dY rows (ctas = 0 where two do not fit, or a thread would own more than
-// eight vectors).
+// four vectors).
 RingPlan dact_ring_plan(int N, bool gated, bool has_z) {
   RingPlan p{};
   const int nv = N / 8;
   const size_t stage = size_t(N) * ((has_z ? 2 : 0) + (gated ? 1 : 2));
   const size_t room = size_t(220) * 1024;
-  p.threads = nv <= 128 ? 128 : 512;
-  p.vpt = (nv + p.threads - 1) / p.threads;
-  p.vpt = p.vpt <= 4 ? p.vpt : (p.vpt <= 6 ? 6 : 8);
+  p.vpt = (nv + 1023) / 1024;
+  p.threads = ring_threads(nv, p.vpt);
+  p.rows = 1;
   p.stages = static_cast<int>(room / stage < size_t(kRingStages) ? room / stage : kRingStages);
-  if (p.stages < 2 || nv > 8 * p.threads) return p;
+  if (p.stages < 2 || p.vpt > 4) return p;
   p.smem = stage * p.stages;
-  const int fit = static_cast<int>(room / p.smem);
-  const int most = p.threads == 128 ? 8 : (p.vpt <= 2 ? 2 : 1);
-  p.ctas = fit < most ? fit : most;
+  p.ctas = ring_ctas(p, 1024);
   return p;
 }
 
@@ -1249,14 +1267,11 @@ FusedBwdLayout fused_bwd_layout(int M, const qlin_weights* w) {
 
 template <bool GATED, bool ACC>
 cudaError_t launch_dact_ring(const RingPlan& p, unsigned grid, const DactArgs& g, cudaStream_t stream) {
-  if (p.threads == 128) return launch_ring(dact_ring_kernel<GATED, 128, 1, ACC>, p, grid, stream, g);
   switch (p.vpt) {
-    case 1: return launch_ring(dact_ring_kernel<GATED, 512, 1, ACC>, p, grid, stream, g);
-    case 2: return launch_ring(dact_ring_kernel<GATED, 512, 2, ACC>, p, grid, stream, g);
-    case 3: return launch_ring(dact_ring_kernel<GATED, 512, 3, ACC>, p, grid, stream, g);
-    case 4: return launch_ring(dact_ring_kernel<GATED, 512, 4, ACC>, p, grid, stream, g);
-    case 6: return launch_ring(dact_ring_kernel<GATED, 512, 6, ACC>, p, grid, stream, g);
-    default: return launch_ring(dact_ring_kernel<GATED, 512, 8, ACC>, p, grid, stream, g);
+    case 1: return launch_ring(dact_ring_kernel<GATED, 1, ACC>, p, grid, stream, g);
+    case 2: return launch_ring(dact_ring_kernel<GATED, 2, ACC>, p, grid, stream, g);
+    case 3: return launch_ring(dact_ring_kernel<GATED, 3, ACC>, p, grid, stream, g);
+    default: return launch_ring(dact_ring_kernel<GATED, 4, ACC>, p, grid, stream, g);
   }
 }
 
@@ -1407,16 +1422,24 @@ cudaError_t launch_norm_t(const NormFwdArgs& g, cudaStream_t stream) {
 
 template <bool ACC>
 cudaError_t launch_norm_backward_ring(const RingPlan& p, unsigned grid, const NormBwdArgs& g, cudaStream_t stream) {
-  if (p.threads == 128) return launch_ring(norm_backward_ring_kernel<128, 1, ACC>, p, grid, stream, g);
-  if (p.threads == 256) return launch_ring(norm_backward_ring_kernel<256, 1, ACC>, p, grid, stream, g);
-  if (p.vpt == 1) return launch_ring(norm_backward_ring_kernel<512, 1, ACC>, p, grid, stream, g);
-  if (p.vpt == 2) return launch_ring(norm_backward_ring_kernel<512, 2, ACC>, p, grid, stream, g);
-  return launch_ring(norm_backward_ring_kernel<512, 4, ACC>, p, grid, stream, g);
+  if (p.vpt == 4) return launch_ring(norm_backward_ring_kernel<4, 1, ACC>, p, grid, stream, g);
+  if (p.vpt == 2)
+    return p.rows == 2 ? launch_ring(norm_backward_ring_kernel<2, 2, ACC>, p, grid, stream, g)
+                       : launch_ring(norm_backward_ring_kernel<2, 1, ACC>, p, grid, stream, g);
+  return p.rows == 4 ? launch_ring(norm_backward_ring_kernel<1, 4, ACC>, p, grid, stream, g)
+                     : launch_ring(norm_backward_ring_kernel<1, 1, ACC>, p, grid, stream, g);
+}
+
+cudaError_t launch_norm_forward_ring(const RingPlan& p, unsigned grid, const NormFwdArgs& g, cudaStream_t stream) {
+  // only calls with more rows than persistent CTAs come here: groups are full
+  if (p.vpt == 4) return launch_ring(norm_forward_ring_kernel<4, 1>, p, grid, stream, g);
+  if (p.vpt == 2) return launch_ring(norm_forward_ring_kernel<2, 2>, p, grid, stream, g);
+  return launch_ring(norm_forward_ring_kernel<1, 4>, p, grid, stream, g);
 }
 
 // Partial rows of dgamma and dbeta: one per CTA of the ring kernel, else one
 // per row group of the column kernel.  The workspace covers both (whether
-// dres is given decides whether a ring fits).
+// dres is given decides whether and how a ring fits).
 struct NormBwdLayout {
   RingPlan ring[2];  // without and with dres
   int G;             // row groups of the column kernel
@@ -1427,7 +1450,7 @@ NormBwdLayout norm_bwd_layout(int M, int K) {
   L.G = column_groups(M, K / 8);
   int most = L.G;
   for (int r = 0; r < 2; ++r) {
-    L.ring[r] = ring_plan(K, 2 + r);
+    L.ring[r] = norm_ring_plan(M, K, 2 + r, true);
     const int n = static_cast<int>(ring_grid(L.ring[r], M));
     if (n > most) most = n;
   }
@@ -1791,15 +1814,11 @@ qlin_status qlin_norm_forward(const uint16_t* X, int32_t M, int32_t K, int32_t k
   const NormFwdArgs g{X, gamma, beta, Y, kind == QLIN_NORM_RMS ? nullptr : mean, rstd, M, K, kind == QLIN_NORM_RMS, eps};
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const int nv = K / 8;
-  const RingPlan ring = ring_plan(K, 1);
+  const RingPlan ring = norm_ring_plan(M, K, 1, false);
   cudaError_t e;
-  if (nv <= 1024 && M > sm_count() * ring.ctas) {  // more rows than one each for the persistent CTAs
-    const unsigned grid = ring_grid(ring, M);
-    if (ring.threads == 128) e = launch_ring(norm_forward_ring_kernel<128, 1>, ring, grid, stream, g);
-    else if (ring.threads == 256) e = launch_ring(norm_forward_ring_kernel<256, 1>, ring, grid, stream, g);
-    else if (ring.vpt == 1) e = launch_ring(norm_forward_ring_kernel<512, 1>, ring, grid, stream, g);
-    else e = launch_ring(norm_forward_ring_kernel<512, 2>, ring, grid, stream, g);
-  } else if (nv <= 32) e = launch_norm_t<32, 1>(g, stream);
+  if (ring.ctas > 0 && M > sm_count() * ring.ctas && ring.rows * ring.vpt == 4)
+    e = launch_norm_forward_ring(ring, ring_grid(ring, M), g, stream);
+  else if (nv <= 32) e = launch_norm_t<32, 1>(g, stream);
   else if (nv <= 128) e = launch_norm_t<32, 4>(g, stream);
   else if (nv <= 512) e = launch_norm_t<128, 4>(g, stream);
   else if (nv <= 1024) e = launch_norm_t<256, 4>(g, stream);
