@@ -31,6 +31,7 @@ struct NormFwdArgs {
   float* rstd;         // [M] or null
   int M, K, rms;
   float eps;
+  int stages;          // ring kernel
 };
 
 struct NormBwdArgs {
@@ -43,6 +44,7 @@ struct NormBwdArgs {
   uint16_t* dX;          // [M][K]
   float* part;           // partial column sums: [G][K] of dgamma, then [G][K] of dbeta; null when none is wanted
   int M, K, rms, G;
+  int stages;            // ring kernel
 };
 
 __device__ __forceinline__ void h8_to_f(const uint4 v, float (&f)[8]) {
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
   const float* p = part + static_cast<size_t>(blockIdx.y) * G * K + k;
   float s = 0.f;
   if (k < K) {
-#pragma unroll 8
+#pragma unroll 16
     for (int i = w; i < G; i += 32) s += p[static_cast<size_t>(i) * K];
   }
   red[w][c] = s;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 // t + T, ... of every row, VPT of them at most (T threads a CTA).  A row
 // costs its element work and a share of a barrier: R rows reduce together,
 // which is what a row at a time spent most of its time on.
-constexpr int kRingStages = 3;
+constexpr int kRingStages = 3;  // at most; two where that lets more CTAs share an SM
 
 // Sums of NV values over the CTA's `nw` warps, returned to every thread.  In
 // the warp, lanes exchange halves of the values (recursive halving), so NV
@@ -300,9 +302,6 @@ __device__ __forceinline__ void ring_load(unsigned char* dst, const uint16_t* a,
   if (c) bulk_load(dst + 2 * next, c + row * K, bytes, bar);
 }
 
-// Shared memory of a ring: the stages of `rows` rows of K values.
-__host__ __device__ inline size_t ring_bytes(int K, int rows) { return size_t(kRingStages) * rows * K * 2; }
-
 __device__ __forceinline__ int group_rows(size_t grp, int R, int M) {  // rows of group grp that exist
   const size_t left = static_cast<size_t>(M) - grp * R;
   return left < static_cast<size_t>(R) ? static_cast<int>(left) : R;
@@ -316,11 +315,11 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const __grid_con
   __shared__ uint64_t full[kRingStages];
   __shared__ int abort_flag;
   const int t = threadIdx.x, T = static_cast<int>(blockDim.x), nw = T >> 5;
-  const int nv = g.K >> 3;
+  const int nv = g.K >> 3, S = g.stages;
   const size_t stage = static_cast<size_t>(R) * g.K * 2;
   const size_t groups = (static_cast<size_t>(g.M) + R - 1) / R, step = gridDim.x;
   if (t == 0) {
-    for (int s = 0; s < kRingStages; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
     abort_flag = 0;
     fence_barrier_init();
   }
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const __grid_con
     ++issued;
   };
   if (t == 0)
-    for (int s = 0; s < kRingStages; ++s)
+    for (int s = 0; s < S; ++s)
       if (blockIdx.x + s * step < groups) load(blockIdx.x + s * step, s);
   f32x2 gm[VPT][4], bt[VPT][4];
 #pragma unroll
@@ -349,10 +348,10 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const __grid_con
   const float invk = 1.f / static_cast<float>(g.K);
   int i = 0;
   for (size_t grp = blockIdx.x; grp < groups; grp += step, ++i) {
-    const int s = i % kRingStages;
+    const int s = i % S;
     const int rows = group_rows(grp, R, g.M);
     const size_t m0 = grp * R;
-    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / kRingStages) & 1u, &abort_flag)) abort_flag = 1;
+    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) abort_flag = 1;
     const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
     f32x2 x[R][VPT][4];  // the rows' values, then x - mu
     float mu[R], q[R];
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const __grid_con
     if (nw == 1) __syncwarp();
     // every thread holds its part of the rows (the sums' barrier): refill
     if (t == 0) {
-      const size_t next = grp + static_cast<size_t>(kRingStages) * step;
+      const size_t next = grp + static_cast<size_t>(S) * step;
       if (abort_flag == 0 && next < groups) load(next, s);
     }
 #pragma unroll
@@ -417,7 +416,7 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const __grid_con
       }
     }
   }
-  if (t == 0 && abort_flag) drain_ring(full, kRingStages, issued);  // no copy outlives the CTA
+  if (t == 0 && abort_flag) drain_ring(full, S, issued);  // no copy outlives the CTA
 }
 
 // Backward over a ring: dX, and with ACC the column sums of dy xh and dy over
@@ -434,12 +433,12 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_co
   __shared__ uint64_t full[kRingStages];
   __shared__ int abort_flag;
   const int t = threadIdx.x, T = static_cast<int>(blockDim.x), nw = T >> 5;
-  const int nv = g.K >> 3;
+  const int nv = g.K >> 3, S = g.stages;
   const size_t part = static_cast<size_t>(R) * g.K * 2;
   const size_t stage = part * (g.dres ? 3 : 2);
   const size_t groups = (static_cast<size_t>(g.M) + R - 1) / R, step = gridDim.x;
   if (t == 0) {
-    for (int s = 0; s < kRingStages; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
     abort_flag = 0;
     fence_barrier_init();
   }
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_co
     ++issued;
   };
   if (t == 0)
-    for (int s = 0; s < kRingStages; ++s)
+    for (int s = 0; s < S; ++s)
       if (blockIdx.x + s * step < groups) load(blockIdx.x + s * step, s);
   f32x2 sg[VPT][4], sb[VPT][4], gk[kGamma ? VPT : 1][4];
 #pragma unroll
@@ -468,18 +467,30 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_co
     }
   }
   const float invk = 1.f / static_cast<float>(g.K);
-  int i = 0;
-  for (size_t grp = blockIdx.x; grp < groups; grp += step, ++i) {
-    const int s = i % kRingStages;
-    const int rows = group_rows(grp, R, g.M);
-    const size_t m0 = grp * R;
-    float mu[R], rs[R];  // read before the wait, so their latency passes with the rows'
+  float mu1[R], rs1[R];  // the next group's statistics, on their way a group ahead
+  auto statistics = [&](size_t grp) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      mu[r] = g.rms || r >= rows ? 0.f : g.mean[m0 + r];
-      rs[r] = r < rows ? g.rstd[m0 + r] : 0.f;
+      const size_t m = grp * R + r;
+      const bool in = m < static_cast<size_t>(g.M);
+      mu1[r] = in && !g.rms ? g.mean[m] : 0.f;
+      rs1[r] = in ? g.rstd[m] : 0.f;
     }
-    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / kRingStages) & 1u, &abort_flag)) abort_flag = 1;
+  };
+  statistics(blockIdx.x);
+  int i = 0;
+  for (size_t grp = blockIdx.x; grp < groups; grp += step, ++i) {
+    const int s = i % S;
+    const int rows = group_rows(grp, R, g.M);
+    const size_t m0 = grp * R;
+    float mu[R], rs[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mu[r] = mu1[r];
+      rs[r] = rs1[r];
+    }
+    statistics(grp + step);
+    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) abort_flag = 1;
     const uint4* dr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
     const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage + part);
     const uint4* rr = reinterpret_cast<const uint4*>(ring_smem + s * stage + 2 * part);
@@ -515,8 +526,8 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_co
     cta_sums<2 * R>(sum, red[i & 1], nw);
     if (nw == 1) __syncwarp();
     if (t == 0 && i > 0 && abort_flag == 0) {  // the previous group's stage
-      const size_t next = grp + static_cast<size_t>(kRingStages - 1) * step;
-      if (next < groups) load(next, (i - 1) % kRingStages);
+      const size_t next = grp + static_cast<size_t>(S - 1) * step;
+      if (next < groups) load(next, (i - 1) % S);
     }
     if (g.dX) {
 #pragma unroll
@@ -544,7 +555,7 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_co
       }
     }
   }
-  if (t == 0 && abort_flag) drain_ring(full, kRingStages, issued);  // no copy outlives the CTA
+  if (t == 0 && abort_flag) drain_ring(full, S, issued);  // no copy outlives the CTA
   if (ACC) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {

@@ -1194,10 +1194,16 @@ RingPlan norm_ring_plan(int M, int K, int arrays, bool backward) {
   p.vpt = nv <= 32 ? 1 : (nv <= 64 || (backward && nv <= 1024) ? 2 : 4);
   p.rows = 4 / p.vpt;
   p.threads = ring_threads(nv, p.vpt);
-  p.stages = kRingStages;
   for (;; p.rows = 1) {
-    p.smem = ring_bytes(K, p.rows * arrays);
+    const size_t stage = size_t(p.rows) * arrays * K * 2;
+    p.stages = kRingStages;
+    p.smem = p.stages * stage;
     p.ctas = ring_ctas(p, 512);
+    RingPlan two = p;
+    two.stages = 2;
+    two.smem = two.stages * stage;
+    two.ctas = ring_ctas(two, 512);
+    if (two.ctas > p.ctas) p = two;
     // one row at a time where groups would leave SMs idle or do not fit
     if (p.rows == 1 || (p.ctas > 0 && (M + p.rows - 1) / p.rows >= sm_count())) break;
   }
@@ -1811,10 +1817,11 @@ qlin_status qlin_norm_forward(const uint16_t* X, int32_t M, int32_t K, int32_t k
   if (!aligned16(X) || !aligned16(gamma) || !aligned16(Y) || (beta && !aligned16(beta)) || (mean && !aligned16(mean)) ||
       (rstd && !aligned16(rstd)))
     return fail(QLIN_ERR_ALIGN, "a norm buffer is not 16-byte aligned");
-  const NormFwdArgs g{X, gamma, beta, Y, kind == QLIN_NORM_RMS ? nullptr : mean, rstd, M, K, kind == QLIN_NORM_RMS, eps};
+  const RingPlan ring = norm_ring_plan(M, K, 1, false);
+  const NormFwdArgs g{X,    gamma, beta, Y, kind == QLIN_NORM_RMS ? nullptr : mean,
+                      rstd, M,     K,    kind == QLIN_NORM_RMS, eps, ring.stages};
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const int nv = K / 8;
-  const RingPlan ring = norm_ring_plan(M, K, 1, false);
   cudaError_t e;
   if (ring.ctas > 0 && M > sm_count() * ring.ctas && ring.rows * ring.vpt == 4)
     e = launch_norm_forward_ring(ring, ring_grid(ring, M), g, stream);
@@ -1856,7 +1863,7 @@ qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M,
   if (!aligned16(dY) || !aligned16(X) || !aligned16(gamma) || !aligned16(rstd) || (mean && !aligned16(mean)) ||
       (dres && !aligned16(dres)) || (dX && !aligned16(dX)))
     return fail(QLIN_ERR_ALIGN, "a norm buffer is not 16-byte aligned");
-  NormBwdArgs g{dY, X, gamma, rms ? nullptr : mean, rstd, dres, dX, nullptr, M, K, rms, 0};
+  NormBwdArgs g{dY, X, gamma, rms ? nullptr : mean, rstd, dres, dX, nullptr, M, K, rms, 0, 0};
   const NormBwdLayout L = norm_bwd_layout(M, K);
   const RingPlan& ring = L.ring[dres ? 1 : 0];
   const bool acc = dgamma || dbeta;
@@ -1868,6 +1875,7 @@ qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M,
   }
   if (ring.ctas > 0) {
     const unsigned grid = ring_grid(ring, M);
+    g.stages = ring.stages;
     cudaError_t e = acc ? launch_norm_backward_ring<true>(ring, grid, g, stream)
                         : launch_norm_backward_ring<false>(ring, grid, g, stream);
     if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "norm_backward_ring_kernel launch failed: %s", cudaGetErrorString(e));
