@@ -4,6 +4,11 @@
 //
 //   relu(z) = max(z, 0)                 relu'  = [z > 0]
 //   gelu(z) = z Phi(z)                  gelu'  = Phi(z) + z phi(z)
+//   with Phi(-x) = exp(-x^2 / 2) P(t), t = 1 / (1 + 0.3 x), for x >= 0 and P a
+//   polynomial of degree 8 without a constant term, fitted to
+//   exp(x^2 / 2) Phi(-x) for the least relative error on [0, 14]: 1.5e-7
+//   (a quarter of what the library's distribution function costs: measured
+//   126 against 59 us for a 1000 x 11008 layer's product and epilogue)
 //   gelu_tanh(z) = z p, p = 1 / (1 + exp(-2 u)), u = sqrt(2/pi) (z + 0.044715 z^3)
 //                                       slope  = p + z p (1 - p) 2 u'
 //   silu(z) = z p, p = 1 / (1 + exp(-z))       = p (1 + z (1 - p))
@@ -39,6 +44,22 @@ __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f
 constexpr float kGeluTanhA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluTanhB = 0.044715f;
 
+// exp(-z^2 / 2) and Phi(z).
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float t = __fdividef(1.f, fmaf(0.3f, fabsf(z), 1.f));
+  e = __expf(-0.5f * z * z);
+  float p = 0.03567487688139828f;
+  p = fmaf(p, t, -0.15720349929292227f);
+  p = fmaf(p, t, 0.2063541956658973f);
+  p = fmaf(p, t, -0.05368424549759451f);
+  p = fmaf(p, t, 0.12856192418724136f);
+  p = fmaf(p, t, 0.09991340876296782f);
+  p = fmaf(p, t, 0.12075396824859583f);
+  p = fmaf(p, t, 0.11962929810635002f);
+  const float q = p * t * e;
+  return z < 0.f ? q : 1.f - q;
+}
+
 // act(z) of N values, the choice made once.
 template <int N>
 __device__ __forceinline__ void act_values(int act, float (&z)[N]) {
@@ -49,7 +70,10 @@ __device__ __forceinline__ void act_values(int act, float (&z)[N]) {
       break;
     case kActGelu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = z[i] * normcdff(z[i]);
+      for (int i = 0; i < N; ++i) {
+        float e;
+        z[i] *= normal_cdf(z[i], e);
+      }
       break;
     case kActGeluTanh:
 #pragma unroll
@@ -77,9 +101,10 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
     case kActGelu:
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float p = normcdff(z[i]);
+        float e;
+        const float p = normal_cdf(z[i], e);
         value[i] = z[i] * p;
-        slope[i] = fmaf(z[i] * 0.3989422804014327f, __expf(-0.5f * z[i] * z[i]), p);
+        slope[i] = fmaf(z[i] * 0.3989422804014327f, e, p);
       }
       break;
     case kActGeluTanh:

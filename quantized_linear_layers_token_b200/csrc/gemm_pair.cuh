@@ -179,8 +179,10 @@ __device__ __forceinline__ int pair_owner(const PairArgs& g, unsigned it) {
 // residual, product, rounding and the stores -- under the next tile's
 // products.
 //   Z first passes through the output tile in shared memory when it is
-// kept; the gated output is 64 channels wide.
-template <int EPI>
+// kept; the gated output is 64 channels wide.  The activation is a template
+// parameter: this code is unrolled over the registers, and five activations
+// in every copy were enough to miss the instruction cache.
+template <int EPI, int ACT>
 __device__ __forceinline__ void pair_epi_tile(const PairParams& prm, unsigned char* smem_y, const float* sa,
                                               float (&v)[8][16], int ctile, int m0, int mvalid, int grp, int nl,
                                               bool issuer) {
@@ -222,29 +224,33 @@ __device__ __forceinline__ void pair_epi_tile(const PairParams& prm, unsigned ch
     if (EPI == kEpiGated) {
       const bool odd = nl & 1;
       float h[8];
-      gated_pair<16>(e.act, v[c], odd, 0xffffffffu, h);
+      gated_pair<16>(ACT, v[c], odd, 0xffffffffu, h);
       const int t0 = c0 + (odd ? 8 : 0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ys[(t0 + i) * 64 + (nl >> 1)] = __half_as_ushort(__float2half_rn(h[i]));
     } else {
-      uint16_t res[16];
+      act_values<16>(ACT, v[c]);
       if (e.residual) {
-        // a warp reads 32 neighbouring channels of one token: two full sectors
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          res[j] = (c0 + j < mvalid && in) ? e.residual[static_cast<size_t>(m0 + c0 + j) * g.N + n] : uint16_t(0);
-      }
-      act_values<16>(e.act, v[c]);
+        for (int h = 0; h < 2; ++h) {
+          uint16_t res[8];  // a warp reads 32 neighbouring channels of one token: two full sectors
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (e.residual) v[c][j] = __fadd_rn(v[c][j], __half2float(__ushort_as_half(res[j])));
-        ys[(c0 + j) * 128 + nl] = __half_as_ushort(__float2half_rn(v[c][j]));
+          for (int j = 0; j < 8; ++j) {
+            const int m = c0 + 8 * h + j;
+            res[j] = (m < mvalid && in) ? e.residual[static_cast<size_t>(m0 + m) * g.N + n] : uint16_t(0);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[c][8 * h + j] = __fadd_rn(v[c][8 * h + j], __half2float(__ushort_as_half(res[j])));
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) ys[(c0 + j) * 128 + nl] = __half_as_ushort(__float2half_rn(v[c][j]));
     }
   }
 }
 
-template <int FMT, int EPI>
+template <int FMT, int EPI, int ACT>
 __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1) gemm_pair_kernel(const __grid_constant__ PairParams prm) {
   using C = PairCfg<FMT>;
   const PairArgs& g = prm.g;
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1) gemm_pair_kernel(co
           if (leader) mbar_arrive(acc_empty);
           else mbar_arrive_remote(lempty);
         }
-        pair_epi_tile<EPI>(prm, smem + C::kOffY, sa, v, ctile, m0, mvalid, grp, nl, issuer);
+        pair_epi_tile<EPI, ACT>(prm, smem + C::kOffY, sa, v, ctile, m0, mvalid, grp, nl, issuer);
         fence_proxy_async_smem();  // the output rows are read by the bulk copy next
         named_bar_sync(1, 256);
         if (issuer && ctile * 128 < g.N) {

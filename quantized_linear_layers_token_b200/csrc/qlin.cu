@@ -247,7 +247,7 @@ struct GemmPlan {
 };
 
 bool use_pair(const GemmPlan& p, const qlin_weights* w);
-template <int FMT, int EPI = kEpiPlain>
+template <int FMT, int EPI = kEpiPlain, int ACT = kActNone>
 int pair_max_clusters();
 
 // Work split of a launch on CTA pairs over `tiles` tiles of T steps (the
@@ -497,12 +497,12 @@ qlin_status launch_gemm_epi(int epi, int bt, GemmParams<1>& prm, cudaStream_t st
 }
 
 // ---------------------------------------------------------------- CTA-pair GEMM (many tokens)
-template <int FMT, int EPI>
+template <int FMT, int EPI, int ACT>
 int pair_max_clusters() {
   static int n = -1;
   static std::once_flag once;
   std::call_once(once, [] {
-    if (cudaFuncSetAttribute(gemm_pair_kernel<FMT, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(gemm_pair_kernel<FMT, EPI, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              PairCfg<FMT>::kSmem) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
@@ -520,7 +520,7 @@ int pair_max_clusters() {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int c = 0;
-    if (cudaOccupancyMaxActiveClusters(&c, gemm_pair_kernel<FMT, EPI>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&c, gemm_pair_kernel<FMT, EPI, ACT>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       c = 0;
     }
@@ -546,7 +546,7 @@ bool use_pair(const GemmPlan& p, const qlin_weights* w) {
 // FMT = kFmtW8: INT8 weight rows by TMA from `codes8` (the INT8 format, or
 // INT4 widened ahead); kFmtW4PC / kFmtW4G128: the layer's packed INT4 codes,
 // converted inside the kernel.
-template <int FMT, int EPI = kEpiPlain>
+template <int FMT, int EPI = kEpiPlain, int ACT = kActNone>
 qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
                              int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream,
                              const EpiArgs* epi = nullptr) {
@@ -573,7 +573,7 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
   g.tiles_m = q.tiles_m;
   g.tiles = g.tiles_n2 * g.tiles_m;
   const double x_bytes = static_cast<double>(M) * w->K;
-  const int maxc = pair_max_clusters<FMT, EPI>();
+  const int maxc = pair_max_clusters<FMT, EPI, ACT>();
   if (maxc < 1) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel: no 2-CTA cluster fits");
   int gm = static_cast<int>(std::lround(std::sqrt(static_cast<double>(maxc) * 256.0 / 256.0)));
   if (x_bytes <= 48.0 * 1024 * 1024) gm = g.tiles_m;
@@ -612,20 +612,35 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
       if (st != QLIN_OK) return st;
     }
   }
-  cudaError_t e = launch_kc(gemm_pair_kernel<FMT, EPI>, dim3(static_cast<unsigned>(2 * g.ncl)),
+  cudaError_t e = launch_kc(gemm_pair_kernel<FMT, EPI, ACT>, dim3(static_cast<unsigned>(2 * g.ncl)),
                             dim3(PairCfg<FMT>::kThreads), PairCfg<FMT>::kSmem, stream, 2, prm);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
+}
+
+// A fused epilogue on CTA pairs, its activation chosen at run time.
+template <int EPI>
+qlin_status launch_pair_act(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
+                            char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream, const EpiArgs* epi) {
+  switch (epi->act) {
+    case kActRelu:
+      return launch_gemm_pair<kFmtW8, EPI, kActRelu>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+    case kActGelu:
+      return launch_gemm_pair<kFmtW8, EPI, kActGelu>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+    case kActGeluTanh:
+      return launch_gemm_pair<kFmtW8, EPI, kActGeluTanh>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+    case kActSilu:
+      return launch_gemm_pair<kFmtW8, EPI, kActSilu>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+    default: return launch_gemm_pair<kFmtW8, EPI, kActNone>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+  }
 }
 
 // INT8 operands on CTA pairs, with the epilogue variant chosen at run time.
 qlin_status launch_pair_w8(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
                            int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream,
                            const EpiArgs* epi, int variant) {
-  if (variant == kEpiGated)
-    return launch_gemm_pair<kFmtW8, kEpiGated>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
-  if (variant == kEpiAct)
-    return launch_gemm_pair<kFmtW8, kEpiAct>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+  if (variant == kEpiGated) return launch_pair_act<kEpiGated>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
+  if (variant == kEpiAct) return launch_pair_act<kEpiAct>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
   return launch_gemm_pair<kFmtW8>(p, w, Xq, a, Y, acc_debug, gws, codes8, cmul, stream);
 }
 
