@@ -289,8 +289,49 @@ void pair_split(GemmPlan& p, long long tiles, int T, int kb, int maxc, bool may_
 // and run the INT8 kernel (QLIN_KNOB_WIDEN_MIN_M; 0 turns it off).
 int widen_min_m() { return static_cast<int>(knob(QLIN_KNOB_WIDEN_MIN_M)); }
 
+// CTAs per tile of a fused launch that has fewer than four tiles per SM: 1
+// for whole tiles, 2, 4 or 8 for ranges that end with the tiles (token tiles
+// of 128 and 256), 0 to leave tiles of up to 64 tokens to the cluster and
+// stream-K splits of the launch.  The least of estimated times in us, from
+// measurements on B200: a pipeline step (512, 256 or 128 inputs of a tile at
+// token tiles of 16, up to 64, above) by format, the exchange of a cluster
+// round, the fix-up of stream-K or of n partial tiles of mv tokens.  At 64
+// tokens of 4096 -> 11008 whole tiles take 16 to 19 us against 26 to 29 split;
+// at 200 tokens 30 to 35 against 69; 11008 -> 4096 at 200 tokens takes 56 to
+// 67 us whole, 50 to 52 in four ranges and 82 to 83 in one per SM.
+int fused_tile_ctas(const GemmProb& g, int bt, int fmt, long long tiles, int sms) {
+  const int f = fmt == QLIN_W4_G128 ? 1 : (fmt == QLIN_W8_PERCHANNEL ? 2 : 0);
+  const double T = g.T;
+  if (bt >= 128) {
+    static const double step[3] = {0.43, 0.57, 0.35};
+    const double mv = g.M < bt ? g.M : bt;
+    int best = 1;
+    double least = T * step[f];
+    for (int n = 2; n <= 8 && n <= g.T && tiles * n <= sms; n *= 2) {
+      const double us = T / n * step[f] + 8.0 + 0.016 * mv * n;
+      if (us < least) {
+        least = us;
+        best = n;
+      }
+    }
+    return best;
+  }
+  static const double step16[3] = {0.53, 1.13, 0.78}, step64[3] = {0.42, 0.70, 0.50};
+  const double st = bt == 16 ? step16[f] : step64[f];
+  const double fixup = bt == 16 ? 8.0 : (bt == 32 ? 15.0 : 21.0);
+  const double round = bt == 16 ? (f == 1 ? 1.2 : 1.8) : (bt == 32 ? 2.0 : 3.7);
+  const double drain = bt == 16 ? 1.0 : (bt == 32 ? 1.5 : 2.0);
+  const double whole = static_cast<double>((tiles + sms - 1) / sms) * (T * st + drain);
+  double split = T * tiles / sms * st + fixup;
+  for (int cs = 2; cs <= 8 && cs <= g.nk; cs *= 2) {
+    const double us = static_cast<double>((tiles + sms / cs - 1) / (sms / cs)) * ((T + cs - 1) / cs * st + round);
+    if (us < split) split = us;
+  }
+  return whole < split ? 1 : 0;
+}
+
 // `fused` launches (a fused epilogue, one problem) keep whole tiles on CTA
-// pairs and widen INT4 ahead of them.
+// pairs, widen INT4 ahead of them, and split tiles by fused_tile_ctas.
 GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused = false) {
   GemmPlan p{};
   p.nprob = n;
@@ -327,7 +368,13 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused
   // Groups of decode problems split too: their tiles differ in length (K),
   // and only split points give every CTA the same number of iterations.
   p.split = (p.tiles < (p.bt >= 128 ? 1LL : 4LL) * sms || (n > 1 && p.bt <= 64)) ? 1 : 0;
-  const long long units = p.split ? iters : p.tiles;
+  long long units = p.split ? iters : p.tiles;
+  // (a forced cluster setting keeps the splits it asks for)
+  if (fused && p.split && sms >= 8 && (p.bt > 64 || !(cluster_disabled() || forced_cluster_size()))) {
+    const int ctas = fused_tile_ctas(p.pr[0], p.bt, ws[0]->fmt, p.tiles, sms);
+    if (ctas == 1) p.split = 0;
+    if (ctas >= 1) units = p.tiles * ctas;  // ranges of one tile each: every ctas-th boundary is a tile start
+  }
   const int cap = sms < kMaxGrid ? sms : kMaxGrid;
   p.grid = static_cast<int>(units < cap ? units : cap);
   if (p.grid < 1) p.grid = 1;

@@ -136,6 +136,14 @@ def test_forward_short_inputs(q, oracle, K):
             check_forward(Layer(q, oracle, fmt, M, K, 176, 3, gated=True), "gelu_tanh", keep_z=True)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_long_inputs(q, oracle, fmt):
+    """Few tiles of many inputs: every token tile cut into ranges."""
+    for M in (1, 20, 60, 100, 200):
+        for gated in (False, True):
+            check_forward(Layer(q, oracle, fmt, M, 8192, 272, 40, gated=gated), "silu", keep_z=True)
+
+
 @pytest.mark.parametrize("act", ref.ACTS)
 def test_every_activation(q, oracle, act):
     """Each activation in each of the four epilogues: cluster split-K,
