@@ -26,7 +26,15 @@
 
 namespace qlin {
 
-constexpr int kColmaxRows = 32;   // rows per CTA of colmax_kernel
+// CTAs of colmax_kernel: about two per SM, from four rows each (32 rows a CTA
+// left most SMs idle up to some 4000 tokens: 12 us at 1000 tokens and 205
+// outlier channels).
+constexpr int kColmaxMinRows = 4;
+constexpr int kColmaxCtas = 296;
+inline int colmax_grid(int M) {
+  const int g = (M + kColmaxMinRows - 1) / kColmaxMinRows;
+  return g < kColmaxCtas ? g : kColmaxCtas;
+}
 constexpr int kQuantThreads = 512;
 constexpr int kFusedMomentumMaxM = 64;  // up to this many tokens the update runs inside quant_kernel
 
@@ -72,8 +80,9 @@ __global__ void colmax_kernel(const uint16_t* __restrict__ X, int M, int K, cons
     scm[i] = 0u;
   }
   __syncthreads();
-  const int r0 = blockIdx.x * kColmaxRows;
-  const int r1 = min(M, r0 + kColmaxRows);
+  // (64-bit: M close to 2^31 would wrap)
+  const int r0 = static_cast<int>(static_cast<long long>(M) * blockIdx.x / gridDim.x);
+  const int r1 = static_cast<int>(static_cast<long long>(M) * (blockIdx.x + 1) / gridDim.x);
   const int total = (r1 - r0) * nO;
   // eight independent gathers per thread in flight before the merges
   const int stride = static_cast<int>(blockDim.x);

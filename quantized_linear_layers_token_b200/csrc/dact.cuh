@@ -32,32 +32,50 @@ struct DactArgs {
   int stages;           // ring kernel
 };
 
-// dZ of 8 channels in fp32 from their packed values: z (8 halves) and dy (8,
-// gated: 4 in x and y).
+// dZ of 8 channels in fp32 pairs from their packed values: z (8 halves) and
+// dy (8, gated: 4 in x and y).
 template <bool GATED>
-__device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv, float (&d)[8]) {
-  float z[8];
-  h8_to_f(zv, z);
+__device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv, f32x2 (&d)[4]) {
+  f32x2 z[4];
+  h8_to_f2(zv, z);
   if (GATED) {
-    const float2 a = __half22float2(u32_as_h2(yv.x)), b = __half22float2(u32_as_h2(yv.y));
-    const float dy[4] = {a.x, a.y, b.x, b.y};
-    const float gate[4] = {z[0], z[2], z[4], z[6]};
-    float val[4], slope[4];
-    act_slopes<4>(act, gate, val, slope);
+    const float2 a = f2_unpack(z[0]), b = f2_unpack(z[1]), c = f2_unpack(z[2]), e = f2_unpack(z[3]);
+    const f32x2 gate[2] = {f2_pack(a.x, b.x), f2_pack(c.x, e.x)};
+    const f32x2 up[2] = {f2_pack(a.y, b.y), f2_pack(c.y, e.y)};
+    const float2 y0 = __half22float2(u32_as_h2(yv.x)), y1 = __half22float2(u32_as_h2(yv.y));
+    const f32x2 dy[2] = {f2_pack(y0.x, y0.y), f2_pack(y1.x, y1.y)};
+    f32x2 val[2], slope[2];
+    act_slopes<2>(act, gate, val, slope);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      d[2 * i] = dy[i] * z[2 * i + 1] * slope[i];
-      d[2 * i + 1] = dy[i] * val[i];
+    for (int i = 0; i < 2; ++i) {
+      const float2 dg = f2_unpack(f2_mul(f2_mul(dy[i], up[i]), slope[i])), du = f2_unpack(f2_mul(dy[i], val[i]));
+      d[2 * i] = f2_pack(dg.x, du.x);
+      d[2 * i + 1] = f2_pack(dg.y, du.y);
     }
   } else {
-    h8_to_f(yv, d);
+    h8_to_f2(yv, d);
     if (act != kActNone) {
-      float val[8], slope[8];
-      act_slopes<8>(act, z, val, slope);
+      f32x2 val[4], slope[4];
+      act_slopes<4>(act, z, val, slope);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] *= slope[i];
+      for (int i = 0; i < 4; ++i) d[i] = f2_mul(d[i], slope[i]);
     }
   }
+}
+
+// dZ m_n 2^e of the channels of vector v in fp16.
+__device__ __forceinline__ uint4 dact_scaled(const f32x2 (&d)[4], float scale, const f32x2 (&mant)[4]) {
+  f32x2 o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = f2_mul(f2_mul(d[i], f2_both(scale)), mant[i]);
+  return f2_to_h8(o);
+}
+__device__ __forceinline__ void load_mant(const DactArgs& g, int v, f32x2 (&m)[4]) {
+  float c[8];
+  load_f8(g.cscale + 8 * v, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m[i] = f2_pack(chan_mant(__fmul_rn(c[2 * i], g.cmul)), chan_mant(__fmul_rn(c[2 * i + 1], g.cmul)));
 }
 
 // A bound on |dZ| of those channels, up to the factor 1.13 of the slopes
@@ -65,13 +83,15 @@ __device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv
 template <bool GATED>
 __device__ __forceinline__ float dact_bound(const uint4 zv, const uint4 yv) {
   if (GATED) {
-    float z[8];
-    h8_to_f(zv, z);
+    const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
     const float2 a = __half22float2(u32_as_h2(yv.x)), b = __half22float2(u32_as_h2(yv.y));
     const float dy[4] = {a.x, a.y, b.x, b.y};
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(dy[i]) * fmaxf(fabsf(z[2 * i]), fabsf(z[2 * i + 1])));
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __habs2(u32_as_h2(zw[i]));
+      top = fmaxf(top, fabsf(dy[i]) * __half2float(__hmax(__low2half(h), __high2half(h))));
+    }
     return top;
   }
   const __half2 m = __hmax2(__hmax2(__habs2(u32_as_h2(yv.x)), __habs2(u32_as_h2(yv.y))),
@@ -129,13 +149,11 @@ __global__ void __launch_bounds__(kDactThreads) dact_rows_kernel(const __grid_co
   if (threadIdx.x == 0) g.rowscale[m] = __uint_as_float((254u - e) << 23);
   for (int v = threadIdx.x; v < nv; v += kDactThreads) {
     uint4 z, y;
-    float d[8], c[8];
+    f32x2 d[4], c[4];
     dact_load<GATED>(g, m, v, z, y);
     dact_vec<GATED>(g.act, z, y, d);
-    load_f8(g.cscale + 8 * v, c);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = (d[i] * scale) * chan_mant(__fmul_rn(c[i], g.cmul));
-    reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = f_to_h8(d);
+    load_mant(g, v, c);
+    reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, c);
   }
 }
 
@@ -147,19 +165,17 @@ __global__ void __launch_bounds__(128) dact_columns_kernel(const __grid_constant
   griddep_wait();
   const int v = blockIdx.x * 128 + threadIdx.x;
   if (v >= (g.N >> 3)) return;
-  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  f32x2 s[4] = {f2_both(0.f), f2_both(0.f), f2_both(0.f), f2_both(0.f)};
 #pragma unroll 2
   for (int m = blockIdx.y; m < g.M; m += g.G) {
     uint4 z, y;
-    float d[8];
+    f32x2 d[4];
     dact_load<GATED>(g, m, v, z, y);
     dact_vec<GATED>(g.act, z, y, d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] += d[i];
+    for (int i = 0; i < 4; ++i) s[i] = f2_add(s[i], d[i]);
   }
-  float4* p = reinterpret_cast<float4*>(g.part + static_cast<size_t>(blockIdx.y) * g.N) + 2 * v;
-  p[0] = make_float4(s[0], s[1], s[2], s[3]);
-  p[1] = make_float4(s[4], s[5], s[6], s[7]);
+  store_f2x4(g.part + static_cast<size_t>(blockIdx.y) * g.N + 8 * v, s);
 }
 
 // Both at once over a row ring (norm.cuh, one row a stage): persistent CTAs of
@@ -203,17 +219,15 @@ __global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__
   if (t == 0)
     for (int s = 0; s < S; ++s)
       if (blockIdx.x + s * step < M) load(blockIdx.x + s * step, s);
-  float sum[ACC ? VPT : 1][8], mant[kKeep ? VPT : 1][8];
+  f32x2 sum[ACC ? VPT : 1][4], mant[kKeep ? VPT : 1][4];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int v = t + j * T;
-    float c[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (kKeep && v < nv) load_f8(g.cscale + 8 * v, c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (ACC) sum[j][e] = 0.f;
-      if (kKeep) mant[j][e] = chan_mant(__fmul_rn(c[e], g.cmul));
+    for (int e = 0; e < 4; ++e) {
+      if (ACC) sum[j][e] = f2_both(0.f);
+      if (kKeep) mant[j][e] = f2_both(0.f);
     }
+    if (kKeep && t + j * T < nv) load_mant(g, t + j * T, mant[kKeep ? j : 0]);
   }
   int i = 0;
   for (size_t m = blockIdx.x; m < M; m += step, ++i) {
@@ -258,24 +272,17 @@ __global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__
       const int v = t + j * T;
       if (v < nv) {
         uint4 z, y;
-        float d[8];
+        f32x2 d[4];
         values(v, z, y);
         dact_vec<GATED>(g.act, z, y, d);
         if (ACC) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[j][e] += d[e];
+          for (int e = 0; e < 4; ++e) sum[j][e] = f2_add(sum[j][e], d[e]);
         }
         if (g.dZ) {
-          if (kKeep) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = (d[e] * scale) * mant[j][e];
-          } else {
-            float c[8];
-            load_f8(g.cscale + 8 * v, c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = (d[e] * scale) * chan_mant(__fmul_rn(c[e], g.cmul));
-          }
-          reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = f_to_h8(d);
+          f32x2 c[4];
+          if (!kKeep) load_mant(g, v, c);
+          reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, kKeep ? mant[kKeep ? j : 0] : c);
         }
       }
     }
@@ -285,11 +292,7 @@ __global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = t + j * T;
-      if (v < nv) {
-        float4* p = reinterpret_cast<float4*>(g.part + static_cast<size_t>(blockIdx.x) * g.N) + 2 * v;
-        p[0] = make_float4(sum[j][0], sum[j][1], sum[j][2], sum[j][3]);
-        p[1] = make_float4(sum[j][4], sum[j][5], sum[j][6], sum[j][7]);
-      }
+      if (v < nv) store_f2x4(g.part + static_cast<size_t>(blockIdx.x) * g.N + 8 * v, sum[j]);
     }
   }
 }

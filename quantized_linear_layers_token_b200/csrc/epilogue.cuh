@@ -13,13 +13,15 @@
 //                                       slope  = p + z p (1 - p) 2 u'
 //   silu(z) = z p, p = 1 / (1 + exp(-z))       = p (1 + z (1 - p))
 // with 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)).  All in fp32; the exponential
-// and the quotient are the hardware approximations (a few units of 2^-22,
+// and the reciprocal are the hardware approximations (a few units of 2^-22,
 // far below half a step of the fp16 results), which reach 0 and z at the
 // ends of the range without an overflow: exp(-2 u) = inf gives p = 0.
 #pragma once
 
 #include <cuda_fp16.h>
 #include <stdint.h>
+
+#include "sm100.cuh"
 
 namespace qlin {
 
@@ -39,30 +41,65 @@ struct EpiArgs {
   int act;
 };
 
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// The arithmetic runs on fp32 pairs (one instruction for two values); the
+// exponential and the reciprocal are a special-function operation a value.
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 ex2_pair(f32x2 x) {
+  const float2 t = f2_unpack(x);
+  return f2_pack(ex2_approx(t.x), ex2_approx(t.y));
+}
+__device__ __forceinline__ f32x2 rcp_pair(f32x2 x) {
+  const float2 t = f2_unpack(x);
+  return f2_pack(rcp_approx(t.x), rcp_approx(t.y));
+}
+// 1 / (1 + 2^x)
+__device__ __forceinline__ f32x2 logistic2(f32x2 x) { return rcp_pair(f2_add(ex2_pair(x), f2_both(1.f))); }
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluTanhA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluTanhB = 0.044715f;
 
-// exp(-z^2 / 2) and Phi(z).
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-  const float t = __fdividef(1.f, fmaf(0.3f, fabsf(z), 1.f));
-  e = __expf(-0.5f * z * z);
-  float p = 0.03567487688139828f;
-  p = fmaf(p, t, -0.15720349929292227f);
-  p = fmaf(p, t, 0.2063541956658973f);
-  p = fmaf(p, t, -0.05368424549759451f);
-  p = fmaf(p, t, 0.12856192418724136f);
-  p = fmaf(p, t, 0.09991340876296782f);
-  p = fmaf(p, t, 0.12075396824859583f);
-  p = fmaf(p, t, 0.11962929810635002f);
-  const float q = p * t * e;
-  return z < 0.f ? q : 1.f - q;
+// z + 0.044715 z^3 and z^2
+__device__ __forceinline__ f32x2 gelu_cubic(f32x2 z, f32x2& z2) {
+  z2 = f2_mul(z, z);
+  return f2_fma(f2_mul(z, f2_both(kGeluTanhB)), z2, z);
 }
 
-// act(z) of N values, the choice made once.
+// exp(-z^2 / 2) and Phi(z).
+__device__ __forceinline__ f32x2 normal_cdf(f32x2 z, f32x2& e) {
+  const float2 v = f2_unpack(z);
+  const f32x2 t = rcp_pair(f2_fma(f2_pack(fabsf(v.x), fabsf(v.y)), f2_both(0.3f), f2_both(1.f)));
+  e = ex2_pair(f2_mul(f2_mul(z, z), f2_both(-0.5f * kLog2e)));
+  f32x2 p = f2_both(0.03567487688139828f);
+  p = f2_fma(p, t, f2_both(-0.15720349929292227f));
+  p = f2_fma(p, t, f2_both(0.2063541956658973f));
+  p = f2_fma(p, t, f2_both(-0.05368424549759451f));
+  p = f2_fma(p, t, f2_both(0.12856192418724136f));
+  p = f2_fma(p, t, f2_both(0.09991340876296782f));
+  p = f2_fma(p, t, f2_both(0.12075396824859583f));
+  p = f2_fma(p, t, f2_both(0.11962929810635002f));
+  const float2 q = f2_unpack(f2_mul(f2_mul(p, t), e));
+  return f2_pack(v.x < 0.f ? q.x : 1.f - q.x, v.y < 0.f ? q.y : 1.f - q.y);
+}
+
+// act(z) of N values (N even), the choice made once.
 template <int N>
 __device__ __forceinline__ void act_values(int act, float (&z)[N]) {
+  static_assert(N % 2 == 0, "values go in pairs");
+  auto put = [&](int i, f32x2 v) {
+    const float2 t = f2_unpack(v);
+    z[i] = t.x;
+    z[i + 1] = t.y;
+  };
   switch (act) {
     case kActRelu:
 #pragma unroll
@@ -70,65 +107,76 @@ __device__ __forceinline__ void act_values(int act, float (&z)[N]) {
       break;
     case kActGelu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float e;
-        z[i] *= normal_cdf(z[i], e);
+      for (int i = 0; i < N; i += 2) {
+        const f32x2 v = f2_pack(z[i], z[i + 1]);
+        f32x2 e;
+        put(i, f2_mul(v, normal_cdf(v, e)));
       }
       break;
     case kActGeluTanh:
 #pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = z[i] * sigmoid_f(kGeluTanhA * fmaf(kGeluTanhB * z[i], z[i] * z[i], z[i]));
+      for (int i = 0; i < N; i += 2) {
+        const f32x2 v = f2_pack(z[i], z[i + 1]);
+        f32x2 z2;
+        put(i, f2_mul(v, logistic2(f2_mul(gelu_cubic(v, z2), f2_both(-kGeluTanhA * kLog2e)))));
+      }
       break;
     case kActSilu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = z[i] * sigmoid_f(z[i]);
+      for (int i = 0; i < N; i += 2) {
+        const f32x2 v = f2_pack(z[i], z[i + 1]);
+        put(i, f2_mul(v, logistic2(f2_mul(v, f2_both(-kLog2e)))));
+      }
       break;
     default: break;
   }
 }
 
-// act(z) and act'(z) of N values.
+// act(z) and act'(z) of N pairs.
 template <int N>
-__device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (&value)[N], float (&slope)[N]) {
+__device__ __forceinline__ void act_slopes(int act, const f32x2 (&z)[N], f32x2 (&value)[N], f32x2 (&slope)[N]) {
+  const f32x2 one = f2_both(1.f);
   switch (act) {
     case kActRelu:
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        value[i] = z[i] < 0.f ? 0.f : z[i];
-        slope[i] = z[i] > 0.f ? 1.f : 0.f;
+        const float2 v = f2_unpack(z[i]);
+        value[i] = f2_pack(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);
+        slope[i] = f2_pack(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
       }
       break;
     case kActGelu:
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float e;
-        const float p = normal_cdf(z[i], e);
-        value[i] = z[i] * p;
-        slope[i] = fmaf(z[i] * 0.3989422804014327f, e, p);
+        f32x2 e;
+        const f32x2 p = normal_cdf(z[i], e);
+        value[i] = f2_mul(z[i], p);
+        slope[i] = f2_fma(f2_mul(z[i], f2_both(0.3989422804014327f)), e, p);
       }
       break;
     case kActGeluTanh:
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float z2 = z[i] * z[i];
-        const float p = sigmoid_f(kGeluTanhA * fmaf(kGeluTanhB * z[i], z2, z[i]));
-        value[i] = z[i] * p;
-        slope[i] = fmaf(z[i] * p * (1.f - p), kGeluTanhA * fmaf(3.f * kGeluTanhB, z2, 1.f), p);
+        f32x2 z2;
+        const f32x2 p = logistic2(f2_mul(gelu_cubic(z[i], z2), f2_both(-kGeluTanhA * kLog2e)));
+        value[i] = f2_mul(z[i], p);
+        const f32x2 q = f2_mul(value[i], f2_fma(p, f2_both(-1.f), one));  // z p (1 - p)
+        slope[i] = f2_fma(q, f2_fma(z2, f2_both(3.f * kGeluTanhA * kGeluTanhB), f2_both(kGeluTanhA)), p);
       }
       break;
     case kActSilu:
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float p = sigmoid_f(z[i]);
-        value[i] = z[i] * p;
-        slope[i] = p * fmaf(z[i], 1.f - p, 1.f);
+        const f32x2 p = logistic2(f2_mul(z[i], f2_both(-kLog2e)));
+        value[i] = f2_mul(z[i], p);
+        slope[i] = f2_fma(value[i], f2_fma(p, f2_both(-1.f), one), p);  // p + z p (1 - p)
       }
       break;
     default:
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         value[i] = z[i];
-        slope[i] = 1.f;
+        slope[i] = one;
       }
   }
 }

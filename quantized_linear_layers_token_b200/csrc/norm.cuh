@@ -100,6 +100,13 @@ __device__ __forceinline__ void load_f2x4(const float* p, f32x2 (&f)[4]) {
   f[2] = f2_pack(b.x, b.y);
   f[3] = f2_pack(b.z, b.w);
 }
+__device__ __forceinline__ void store_f2x4(float* p, const f32x2 (&f)[4]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float2 a = f2_unpack(f[2 * e]), b = f2_unpack(f[2 * e + 1]);
+    reinterpret_cast<float4*>(p)[e] = make_float4(a.x, a.y, b.x, b.y);
+  }
+}
 __device__ __forceinline__ float f2_sum(f32x2 v) {
   const float2 t = f2_unpack(v);
   return t.x + t.y;
@@ -561,15 +568,8 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_co
     for (int j = 0; j < VPT; ++j) {
       const int v = t + j * T;
       if (v < nv) {
-        float4* pg = reinterpret_cast<float4*>(g.part + static_cast<size_t>(blockIdx.x) * g.K) + 2 * v;
-        float4* pb = reinterpret_cast<float4*>(g.part + (step + blockIdx.x) * g.K) + 2 * v;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 a = f2_unpack(sg[j][2 * e]), b = f2_unpack(sg[j][2 * e + 1]);
-          const float2 c = f2_unpack(sb[j][2 * e]), d = f2_unpack(sb[j][2 * e + 1]);
-          pg[e] = make_float4(a.x, a.y, b.x, b.y);
-          pb[e] = make_float4(c.x, c.y, d.x, d.y);
-        }
+        store_f2x4(g.part + static_cast<size_t>(blockIdx.x) * g.K + 8 * v, sg[j]);
+        store_f2x4(g.part + (step + blockIdx.x) * g.K + 8 * v, sb[j]);
       }
     }
   }
