@@ -78,6 +78,18 @@ __device__ __forceinline__ void load_mant(const DactArgs& g, int v, f32x2 (&m)[4
     m[i] = f2_pack(chan_mant(__fmul_rn(c[2 * i], g.cmul)), chan_mant(__fmul_rn(c[2 * i + 1], g.cmul)));
 }
 
+// The same where chan_mant_is_fraction holds (a power of two in cmul changes
+// no fraction): one logic operation a value.
+__device__ __forceinline__ float fraction(float c) {
+  return __uint_as_float((__float_as_uint(c) & 0x007FFFFFu) | 0x3F800000u);
+}
+__device__ __forceinline__ void load_fraction(const DactArgs& g, int v, f32x2 (&m)[4]) {
+  float c[8];
+  load_f8(g.cscale + 8 * v, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = f2_pack(fraction(c[2 * i]), fraction(c[2 * i + 1]));
+}
+
 // A bound on |dZ| of those channels, up to the factor 1.13 of the slopes
 // (and |act(z)| <= |z|).
 template <bool GATED>
@@ -122,6 +134,7 @@ __device__ __forceinline__ void dact_load(const DactArgs& g, size_t m, int v, ui
 }
 
 constexpr int kDactThreads = 512;
+constexpr int kDactRingThreads = 768;  // at most: 80 registers a thread
 
 // One CTA per token row: the row's scale from the bound, then dZ in one more
 // pass over the row.
@@ -186,8 +199,8 @@ __global__ void __launch_bounds__(128) dact_columns_kernel(const __grid_constant
 // as partial row blockIdx.x.  dZ is skipped when it is null (only the bias's
 // gradient is wanted).
 template <bool GATED, int VPT, bool ACC>
-__global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__ DactArgs g) {
-  constexpr bool kKeep = VPT * (ACC ? 2 : 1) <= 3;
+__global__ void __launch_bounds__(kDactRingThreads) dact_ring_kernel(const __grid_constant__ DactArgs g) {
+  constexpr bool kKeep = VPT * (ACC ? 2 : 1) <= 4;
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ float red[2][32];
   __shared__ uint64_t full[kRingStages];
@@ -195,7 +208,7 @@ __global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__
   const int t = threadIdx.x, T = static_cast<int>(blockDim.x), nw = T >> 5;
   const int nv = g.N >> 3;
   const bool has_z = GATED || g.act != kActNone;
-  const uint32_t zb = has_z ? static_cast<uint32_t>(g.N) * 2u : 0u;
+  const uint32_t zb = has_z ? static_cast<uint32_t>(g.N) * 2u : 0u;  // bytes of a row
   const uint32_t yb = static_cast<uint32_t>(g.N) * (GATED ? 1u : 2u);
   const size_t stage = zb + yb;
   const int S = g.stages;
@@ -220,6 +233,7 @@ __global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__
     for (int s = 0; s < S; ++s)
       if (blockIdx.x + s * step < M) load(blockIdx.x + s * step, s);
   f32x2 sum[ACC ? VPT : 1][4], mant[kKeep ? VPT : 1][4];
+  bool inside = true;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
 #pragma unroll
@@ -227,8 +241,19 @@ __global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__
       if (ACC) sum[j][e] = f2_both(0.f);
       if (kKeep) mant[j][e] = f2_both(0.f);
     }
-    if (kKeep && t + j * T < nv) load_mant(g, t + j * T, mant[kKeep ? j : 0]);
+    if (t + j * T < nv) {
+      if (kKeep) {
+        load_mant(g, t + j * T, mant[kKeep ? j : 0]);
+      } else {
+        float c[8];
+        load_f8(g.cscale + 8 * (t + j * T), c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) inside = inside && chan_mant_is_fraction(__fmul_rn(c[e], g.cmul));
+      }
+    }
   }
+  // the usual case: every channel factor's mantissa is its fraction field
+  if (!kKeep) inside = __syncthreads_and(inside);
   int i = 0;
   for (size_t m = blockIdx.x; m < M; m += step, ++i) {
     const int s = i % S;
@@ -281,7 +306,10 @@ __global__ void __launch_bounds__(1024) dact_ring_kernel(const __grid_constant__
         }
         if (g.dZ) {
           f32x2 c[4];
-          if (!kKeep) load_mant(g, v, c);
+          if (!kKeep) {
+            if (inside) load_fraction(g, v, c);
+            else load_mant(g, v, c);
+          }
           reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, kKeep ? mant[kKeep ? j : 0] : c);
         }
       }

@@ -24,6 +24,7 @@
 #pragma once
 
 #include "backward.cuh"
+#include "norm.cuh"
 
 namespace qlin {
 
@@ -38,6 +39,12 @@ __device__ __forceinline__ float chan_pow2(float c) {
 __device__ __forceinline__ float chan_mant(float c) {  // exact
   const uint32_t k = __float_as_uint(chan_pow2(c)) >> 23;
   return __fmul_rn(c, __uint_as_float((254u - k) << 23));
+}
+
+// m_n in [1, 2): the fraction field of c'_n.
+__device__ __forceinline__ bool chan_mant_is_fraction(float c) {
+  const uint32_t e = (__float_as_uint(c) >> 23) & 0xFFu;
+  return e >= 113u && e <= 135u;
 }
 
 // c'_n of the forward's INT8 operand: c_n / 16 for per-channel INT4 (16 q), else c_n.
@@ -55,6 +62,10 @@ struct DxWidenArgs {
   const float* s;
   uint8_t* out;  // operand blocks [ceil(K / 128)][nst] of 16 KiB
   int N, nO, kb, nst, nib;
+  // the CTAs behind the blocks sum the bias gradient's partial rows (null: none)
+  const float* part;
+  float* dbias;
+  int blocks, G;
 };
 
 // One CTA per packed block of 128 channels x 128 inputs, two operand blocks
@@ -63,12 +74,19 @@ struct DxWidenArgs {
 // tensor core's 128-byte swizzle (inputs contiguous: the packed rows'
 // direction, so nothing is transposed).  The blocks are put together in
 // shared memory, eight threads a row, the outlier inputs are blended there
-// by two threads a row, and one bulk copy each takes them out.
+// by two threads a row, and one bulk copy each takes them out.  The column
+// sums of the bias's gradient ride along in CTAs of their own: alone they are
+// a launch that waits for a few loads.
 template <int FMT>
 __global__ void __launch_bounds__(256) dx_widen_kernel(const __grid_constant__ DxWidenArgs g) {
   __shared__ __align__(128) unsigned char blk[32768];
   __shared__ int first, count;  // the block's outliers: consecutive entries of the sorted list
   griddep_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= g.blocks) {
+    griddep_wait();
+    column_sum<8>(g.part, g.G, g.N, static_cast<int>(blockIdx.x) - g.blocks, g.dbias);
+    return;
+  }
   const int tn = static_cast<int>(blockIdx.x) / g.kb;
   const int kb = static_cast<int>(blockIdx.x) - tn * g.kb;
   const uint8_t* src = g.codes + static_cast<size_t>(blockIdx.x) * (FMT == kFmtW8 ? 16384 : 8192);

@@ -224,29 +224,38 @@ __global__ void __launch_bounds__(128) norm_columns_kernel(const __grid_constant
   pb[1] = make_float4(sb[4], sb[5], sb[6], sb[7]);
 }
 
-// out[k] = sum over the G partial rows, in one order: 32 warps take the rows
-// w, w + 32, ... of 32 columns, and their sums are added in order.
-// blockIdx.y selects dgamma (0) or dbeta (1).
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part, int G, int K,
-                                                          float* __restrict__ out0, float* __restrict__ out1) {
-  __shared__ float red[32][33];
-  griddep_launch_dependents();
-  griddep_wait();
-  float* out = blockIdx.y ? out1 : out0;
-  if (!out) return;
+// out[k] = sum over the G partial rows of part [G][K], in one order: the W
+// warps of the CTA take the rows w, w + W, ... of 32 columns, and their sums
+// are added in order.
+template <int W>
+__device__ __forceinline__ void column_sum(const float* __restrict__ part, int G, int K, int block,
+                                           float* __restrict__ out) {
+  __shared__ float red[W][32];
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int k = blockIdx.x * 32 + c;
-  const float* p = part + static_cast<size_t>(blockIdx.y) * G * K + k;
+  const int k = block * 32 + c;
+  const float* p = part + k;
   float s = 0.f;
   if (k < K) {
 #pragma unroll 16
-    for (int i = w; i < G; i += 32) s += p[static_cast<size_t>(i) * K];
+    for (int i = w; i < G; i += W) s += __ldcg(p + static_cast<size_t>(i) * K);
   }
   red[w][c] = s;
   __syncthreads();
-  // warp w adds the 32 sums of column w, a lane each
-  s = warp_sum(red[c][w]);
-  if (c == 0 && static_cast<int>(blockIdx.x) * 32 + w < K) out[blockIdx.x * 32 + w] = s;
+  if (w == 0 && k < K) {
+#pragma unroll
+    for (int i = 1; i < W; ++i) s += red[i][c];
+    out[k] = s;
+  }
+}
+
+// dgamma (blockIdx.y = 0) and dbeta (1) from part [2][G][K]; either may be null.
+template <int W>
+__global__ void __launch_bounds__(32 * W) column_sum_kernel(const float* __restrict__ part, int G, int K,
+                                                          float* __restrict__ out0, float* __restrict__ out1) {
+  griddep_launch_dependents();
+  griddep_wait();
+  float* out = blockIdx.y ? out1 : out0;
+  if (out) column_sum<W>(part + static_cast<size_t>(blockIdx.y) * G * K, G, K, static_cast<int>(blockIdx.x), out);
 }
 
 // ---- Row rings: persistent CTAs work through groups of R neighbouring rows,

@@ -1165,9 +1165,10 @@ int column_groups(int M, int nv) {
 
 // Partial column sums [G][K] (twice that, dgamma then dbeta, for a norm) to
 // their totals.
+template <int W>
 qlin_status launch_column_sum(const float* part, int G, int K, float* out0, float* out1, cudaStream_t stream) {
-  cudaError_t e = launch_k(column_sum_kernel, dim3((K + 31) / 32, out1 ? 2 : 1), dim3(1024), 0, stream, part, G, K, out0,
-                           out1);
+  cudaError_t e = launch_k(column_sum_kernel<W>, dim3((K + 31) / 32, out1 ? 2 : 1), dim3(32 * W), 0, stream, part, G, K,
+                           out0, out1);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "column_sum_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
 }
@@ -1220,7 +1221,7 @@ DxPlan plan_dx(int M, const qlin_weights* w) {
   double best = 0.0;
   for (int S = 1; S <= 16 && S <= p.nst; ++S) {
     const double waves = static_cast<double>((tiles * S + pairs - 1) / pairs);
-    const double traffic = S > 1 ? 8.0 * S * M * w->K / 1.7e6 + 10.0 : 0.0;  // bytes over about 6 TB/s, in steps
+    const double traffic = S > 1 ? 8.0 * S * M * w->K / 1.7e6 + 20.0 : 0.0;  // bytes over about 6 TB/s and a launch, in steps
     const double cost = waves * ((p.nst + S - 1) / S + 8.0) + traffic;
     if (S == 1 || cost < best) {
       best = cost;
@@ -1292,21 +1293,21 @@ unsigned ring_grid(const RingPlan& p, int M) {
   return static_cast<unsigned>(groups < most ? groups : most);
 }
 
-// The ring of the activation's backward pass: two or three stages of Z and
-// dY rows (ctas = 0 where two do not fit, or a thread would own more than
-// four vectors).
+// The ring of the activation's backward pass: two or three stages of a Z and
+// a dY row (ctas = 0 where two do not fit, or a thread would own more than
+// six vectors).
 RingPlan dact_ring_plan(int N, bool gated, bool has_z) {
   RingPlan p{};
   const int nv = N / 8;
   const size_t stage = size_t(N) * ((has_z ? 2 : 0) + (gated ? 1 : 2));
   const size_t room = size_t(220) * 1024;
-  p.vpt = (nv + 1023) / 1024;
+  p.vpt = (nv + kDactRingThreads - 1) / kDactRingThreads;
   p.threads = ring_threads(nv, p.vpt);
   p.rows = 1;
   p.stages = static_cast<int>(room / stage < size_t(kRingStages) ? room / stage : kRingStages);
-  if (p.stages < 2 || p.vpt > 4) return p;
+  if (p.stages < 2 || p.vpt > 6) return p;
   p.smem = stage * p.stages;
-  p.ctas = ring_ctas(p, 1024);
+  p.ctas = ring_ctas(p, kDactRingThreads);
   return p;
 }
 
@@ -1345,14 +1346,16 @@ cudaError_t launch_dact_ring(const RingPlan& p, unsigned grid, const DactArgs& g
     case 1: return launch_ring(dact_ring_kernel<GATED, 1, ACC>, p, grid, stream, g);
     case 2: return launch_ring(dact_ring_kernel<GATED, 2, ACC>, p, grid, stream, g);
     case 3: return launch_ring(dact_ring_kernel<GATED, 3, ACC>, p, grid, stream, g);
-    default: return launch_ring(dact_ring_kernel<GATED, 4, ACC>, p, grid, stream, g);
+    case 4: return launch_ring(dact_ring_kernel<GATED, 4, ACC>, p, grid, stream, g);
+    case 5: return launch_ring(dact_ring_kernel<GATED, 5, ACC>, p, grid, stream, g);
+    default: return launch_ring(dact_ring_kernel<GATED, 6, ACC>, p, grid, stream, g);
   }
 }
 
 template <int FMT>
-cudaError_t launch_dx_widen(const DxWidenArgs& a, int tiles_n, cudaStream_t stream) {
-  return launch_k(dx_widen_kernel<FMT>, dim3(static_cast<unsigned>(tiles_n) * static_cast<unsigned>(a.kb)), dim3(256), 0,
-                  stream, a);
+cudaError_t launch_dx_widen(const DxWidenArgs& a, cudaStream_t stream) {
+  const unsigned sums = a.dbias ? static_cast<unsigned>((a.N + 31) / 32) : 0u;
+  return launch_k(dx_widen_kernel<FMT>, dim3(static_cast<unsigned>(a.blocks) + sums), dim3(256), 0, stream, a);
 }
 
 // dX from the scaled dZ and the widened operand.
@@ -1437,29 +1440,26 @@ qlin_status backward_fused(const qlin_weights* w, const uint16_t* dY, const uint
   g.G = L.G;
   const RingPlan ring = dact_ring_plan(w->N, GATED, needs_z);
   cudaError_t e;
+  int parts = L.G;  // partial rows of the bias's gradient
   if (ring.ctas > 0) {
     const unsigned grid = ring_grid(ring, M);
     g.stages = ring.stages;
     if (!dX) g.dZ = nullptr;
     e = dbias ? launch_dact_ring<GATED, true>(ring, grid, g, stream) : launch_dact_ring<GATED, false>(ring, grid, g, stream);
     if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_ring_kernel launch failed: %s", cudaGetErrorString(e));
-    if (dbias) {
-      st = launch_column_sum(g.part, static_cast<int>(grid), w->N, dbias, nullptr, stream);
-      if (st != QLIN_OK) return st;
-    }
+    parts = static_cast<int>(grid);
   } else {
     if (dbias) {
       e = launch_k(dact_columns_kernel<GATED>, dim3((w->N / 8 + 127) / 128, L.G), dim3(128), 0, stream, g);
       if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_columns_kernel launch failed: %s", cudaGetErrorString(e));
-      st = launch_column_sum(g.part, L.G, w->N, dbias, nullptr, stream);
-      if (st != QLIN_OK) return st;
     }
     if (dX) {
       e = launch_k(dact_rows_kernel<GATED>, dim3(static_cast<unsigned>(M)), dim3(kDactThreads), 0, stream, g);
       if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dact_rows_kernel launch failed: %s", cudaGetErrorString(e));
     }
   }
-  if (!dX) return QLIN_OK;
+  // eight warps: the order in which the widening kernel adds them
+  if (!dX) return launch_column_sum<8>(g.part, parts, w->N, dbias, nullptr, stream);
   DxWidenArgs a{};
   a.codes = static_cast<const uint8_t*>(w->codes);
   a.rfold = w->fold_ratio;
@@ -1473,10 +1473,13 @@ qlin_status backward_fused(const qlin_weights* w, const uint16_t* dY, const uint
   a.kb = (w->K + 127) / 128;
   a.nst = L.dx.nst;
   a.nib = (nO + 63) / 64;
-  const int tiles_n = (w->N + 127) / 128;
-  e = w->fmt == QLIN_W4_PERCHANNEL ? launch_dx_widen<kFmtW4PC>(a, tiles_n, stream)
-      : w->fmt == QLIN_W4_G128     ? launch_dx_widen<kFmtW4G128>(a, tiles_n, stream)
-                                   : launch_dx_widen<kFmtW8>(a, tiles_n, stream);
+  a.part = g.part;
+  a.dbias = dbias;
+  a.blocks = (w->N + 127) / 128 * a.kb;
+  a.G = parts;
+  e = w->fmt == QLIN_W4_PERCHANNEL ? launch_dx_widen<kFmtW4PC>(a, stream)
+      : w->fmt == QLIN_W4_G128     ? launch_dx_widen<kFmtW4G128>(a, stream)
+                                   : launch_dx_widen<kFmtW8>(a, stream);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dx_widen_kernel launch failed: %s", cudaGetErrorString(e));
   return launch_dx(w, M, L, ws, dX, stream);
 }
@@ -1947,14 +1950,14 @@ qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M,
     cudaError_t e = acc ? launch_norm_backward_ring<true>(ring, grid, g, stream)
                         : launch_norm_backward_ring<false>(ring, grid, g, stream);
     if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "norm_backward_ring_kernel launch failed: %s", cudaGetErrorString(e));
-    return acc ? launch_column_sum(g.part, static_cast<int>(grid), K, dgamma, dbeta, stream) : QLIN_OK;
+    return acc ? launch_column_sum<32>(g.part, static_cast<int>(grid), K, dgamma, dbeta, stream) : QLIN_OK;
   }
   if (acc) {
     g.G = L.G;
     // before dX, which may replace dY or X
     cudaError_t e = launch_k(norm_columns_kernel, dim3((K / 8 + 127) / 128, L.G), dim3(128), 0, stream, g);
     if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "norm_columns_kernel launch failed: %s", cudaGetErrorString(e));
-    st = launch_column_sum(g.part, L.G, K, dgamma, dbeta, stream);
+    st = launch_column_sum<32>(g.part, L.G, K, dgamma, dbeta, stream);
     if (st != QLIN_OK) return st;
   }
   if (!dX) return QLIN_OK;
