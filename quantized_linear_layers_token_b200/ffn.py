@@ -1,0 +1,113 @@
+"""The feed-forward half of a transformer block on packed quantized weights:
+
+    y = x + W_down (act(W_gate n(x)) * (W_up n(x)))
+
+with n a layer norm or an RMS norm, for serving (one token and up) and for
+fine-tuning over the frozen weights.  Four library calls forward
+(:func:`qlin.qlin_norm_forward`, :func:`qlin.qlin_forward_gated`,
+:func:`qlin.qlin_forward_act` with the residual), three backward; PyTorch
+holds the memory and nothing else.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import qlin
+
+
+@dataclass
+class Saved:
+    """What a training forward keeps for its backward pass."""
+    x: torch.Tensor        # [M][D]
+    mean: torch.Tensor     # [M], None for the RMS norm
+    rstd: torch.Tensor     # [M]
+    z: torch.Tensor        # [M][2 F] pre-activations, gate and up alternating
+    s_gated: torch.Tensor  # the scales this forward quantized with
+    s_down: torch.Tensor
+
+
+class GatedFeedForward:
+    """`gated` is packed by ``PackedLayer.pack_gated`` ([D] -> 2 [F]), `down`
+    by ``PackedLayer.pack`` ([F] -> [D]).  gamma, beta and the biases are fp32
+    (`bias_gated` in the packed order); beta and the biases may be None.
+
+    A training forward updates both momentum states (`s_gated`, `s_down`) and
+    returns what its backward pass needs; several may be outstanding.  Calls of
+    one object run one after the other on one stream (they share workspaces),
+    replays of captured calls among them.  Workspaces change with the token
+    count; those that a captured call uses are kept for the object's life, so a
+    captured graph may be replayed as long as the object lives.
+    """
+
+    def __init__(self, gated: qlin.PackedLayer, down: qlin.PackedLayer, gamma, beta=None, bias_gated=None,
+                 bias_down=None, kind: int = qlin.QLIN_NORM_RMS, eps: float = 1e-5, act: int = qlin.QLIN_ACT_SILU,
+                 momentum: float = 0.9):
+        if gated.K != down.N or gated.N != 2 * down.K:
+            raise ValueError(f"gated [{gated.K}] -> [{gated.N}] and down [{down.K}] -> [{down.N}] do not fit together")
+        self.gated, self.down = gated, down
+        self.D, self.F = down.N, down.K
+        self.gamma, self.beta, self.bias_gated, self.bias_down = gamma, beta, bias_gated, bias_down
+        self.kind, self.eps, self.act, self.momentum = kind, eps, act, momentum
+        dev = gated.buffer.device
+        self.s_gated = torch.ones(gated.n_outlier, device=dev)
+        self.s_down = torch.ones(down.n_outlier, device=dev)
+        self._ws = {}        # name -> (workspace, token count) of the last call
+        self._captured = {}  # (name, token count) -> workspace of captured calls
+
+    def _workspace(self, name: str, nbytes: int, M: int):
+        """A zero-filled buffer that belongs to one token count: what a call
+        leaves zero lies elsewhere at another count."""
+        ws = self._captured.get((name, M))
+        if ws is None:
+            ws, n = self._ws.get(name, (None, -1))
+            if n != M or ws.numel() < nbytes:
+                ws = qlin.empty_workspace(nbytes, device=self.gated.buffer.device)
+                self._ws[name] = (ws, M)
+            if torch.cuda.is_current_stream_capturing():
+                self._captured[name, M] = ws
+        return ws, nbytes
+
+    def _half(self, *shape):
+        return torch.empty(shape, dtype=torch.float16, device=self.gated.buffer.device)
+
+    def forward(self, x: torch.Tensor, training: bool = False):
+        """y [M][D] of x fp16 [M][D]; with `training`, (y, Saved)."""
+        M = x.shape[0]
+        n, h, y = self._half(M, self.D), self._half(M, self.F), self._half(M, self.D)
+        z = self._half(M, 2 * self.F) if training else None
+        f32 = dict(dtype=torch.float32, device=n.device)
+        mean = torch.empty(M, **f32) if training and self.kind == qlin.QLIN_NORM_LAYER else None
+        rstd = torch.empty(M, **f32) if training else None
+        qlin.qlin_norm_forward(x, M, self.D, self.kind, self.gamma, self.beta, self.eps, n, mean, rstd)
+        ws, nws = self._workspace("gated", qlin.qlin_forward_gated_workspace(M, self.gated.w), M)
+        qlin.qlin_forward_gated(n, M, self.gated.w, self.s_gated, self.momentum, training, h, ws, nws, act=self.act,
+                                bias=self.bias_gated, Z=z)
+        ws, nws = self._workspace("down", qlin.qlin_forward_act_workspace(M, self.down.w), M)
+        qlin.qlin_forward_act(h, M, self.down.w, self.s_down, self.momentum, training, y, ws, nws,
+                              bias=self.bias_down, residual=x)
+        if not training:
+            return y
+        return y, Saved(x, mean, rstd, z, self.s_gated.clone(), self.s_down.clone())
+
+    def backward(self, saved: Saved, dy: torch.Tensor) -> dict:
+        """Gradients of x and of the trainable vectors (None where there is
+        no such vector): dx, dgamma, dbeta, dbias_gated, dbias_down."""
+        M = dy.shape[0]
+        dev = self.gated.buffer.device
+        dh, dn, dx = self._half(M, self.F), self._half(M, self.D), self._half(M, self.D)
+
+        def like(v, n):
+            return None if v is None else torch.empty(n, dtype=torch.float32, device=dev)
+
+        dbg, dbd = like(self.bias_gated, 2 * self.F), like(self.bias_down, self.D)
+        dgamma, dbeta = like(self.gamma, self.D), like(self.beta, self.D)
+        nws = max(qlin.qlin_backward_act_workspace(M, self.down.w), qlin.qlin_backward_gated_workspace(M, self.gated.w),
+                  qlin.qlin_norm_backward_workspace(M, self.D))
+        ws, _ = self._workspace("backward", nws, M)
+        qlin.qlin_backward_act(self.down.w, dy, None, M, saved.s_down, dh, dbd, ws, nws)
+        qlin.qlin_backward_gated(self.gated.w, dh, saved.z, M, saved.s_gated, dn, dbg, ws, nws, act=self.act)
+        qlin.qlin_norm_backward(dn, saved.x, M, self.D, self.kind, self.gamma, saved.mean, saved.rstd, dy, dx, dgamma,
+                                dbeta, ws, nws)
+        return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta, "dbias_gated": dbg, "dbias_down": dbd}
