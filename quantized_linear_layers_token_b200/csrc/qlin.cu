@@ -191,6 +191,21 @@ cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
   return launch_kc(kern, grid, block, smem, stream, 1, args...);
 }
 
+// Raise a kernel's shared-memory limit, once on each device (the attribute
+// belongs to the device's context).
+template <auto Kern>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 int sm_count() {
   static int cached[64] = {};
   int dev = 0;
@@ -448,11 +463,7 @@ template <int FMT, int BT, int MAXP, int EPI>
 qlin_status launch_gemm_t(GemmParams<MAXP>& prm, cudaStream_t stream) {
   using C = GemmCfg<FMT, BT>;
   auto kern = gemm_kernel<FMT, BT, MAXP, EPI>;
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  });
+  const cudaError_t attr_err = allow_smem<gemm_kernel<FMT, BT, MAXP, EPI>>(C::kSmemBytes);
   if (attr_err != cudaSuccess) return fail(QLIN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
   GemmArgs& args = prm.g;
   // Single-problem launches whose token tiles (up to 64) would be split
@@ -665,7 +676,9 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
       if (st != QLIN_OK) return st;
     }
   }
-  cudaError_t e = launch_kc(gemm_pair_kernel<FMT, EPI, ACT>, dim3(static_cast<unsigned>(2 * g.ncl)),
+  cudaError_t e = allow_smem<gemm_pair_kernel<FMT, EPI, ACT>>(PairCfg<FMT>::kSmem);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel attribute: %s", cudaGetErrorString(e));
+  e = launch_kc(gemm_pair_kernel<FMT, EPI, ACT>, dim3(static_cast<unsigned>(2 * g.ncl)),
                             dim3(PairCfg<FMT>::kThreads), PairCfg<FMT>::kSmem, stream, 2, prm);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
@@ -838,9 +851,7 @@ struct QuantIO {
 template <int VPT, bool FUSED, int MAXP>
 qlin_status launch_quant_v(const QuantGroup<MAXP>& qg, int rows, size_t smem, cudaStream_t stream) {
   auto kern = quant_kernel<VPT, FUSED, MAXP>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] { attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQuantSmemMax); });
+  const cudaError_t attr = allow_smem<quant_kernel<VPT, FUSED, MAXP>>(kQuantSmemMax);
   if (attr != cudaSuccess) return fail(QLIN_ERR_CUDA, "quant_kernel attribute: %s", cudaGetErrorString(attr));
   cudaError_t e = launch_k(kern, dim3(rows), dim3(kQuantThreads), smem, stream, qg);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "quant_kernel launch failed: %s", cudaGetErrorString(e));
@@ -1235,6 +1246,8 @@ DxPlan plan_dx(int M, const qlin_weights* w) {
   return p;
 }
 
+constexpr int kRingRoom = 220 * 1024;  // of an SM's shared memory, for every ring on it
+
 // A row ring's shape: threads, vectors per thread, rows per group, stages and
 // persistent CTAs per SM (0 where the ring does not fit).
 struct RingPlan {
@@ -1246,7 +1259,7 @@ struct RingPlan {
 int ring_threads(int nv, int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; }
 
 int ring_ctas(const RingPlan& p, int threads_per_sm) {
-  const int fit = static_cast<int>(size_t(220) * 1024 / p.smem);
+  const int fit = static_cast<int>(kRingRoom / p.smem);
   int most = threads_per_sm / p.threads;
   if (most > 16) most = 16;  // more would only lengthen the sums over the CTAs
   return fit < most ? fit : most;
@@ -1279,12 +1292,11 @@ RingPlan norm_ring_plan(int M, int K, int arrays, bool backward) {
   return p;
 }
 
-template <typename Args>
-cudaError_t launch_ring(void (*kern)(Args), const RingPlan& p, unsigned grid, cudaStream_t stream, const Args& g) {
-  // raising a kernel's shared-memory limit is idempotent and needs no stream
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.smem));
+template <auto Kern, typename Args>
+cudaError_t launch_ring(const RingPlan& p, unsigned grid, cudaStream_t stream, const Args& g) {
+  cudaError_t e = allow_smem<Kern>(kRingRoom);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(grid), dim3(p.threads), p.smem, stream, g);
+  return launch_k(Kern, dim3(grid), dim3(p.threads), p.smem, stream, g);
 }
 
 unsigned ring_grid(const RingPlan& p, int M) {
@@ -1300,7 +1312,7 @@ RingPlan dact_ring_plan(int N, bool gated, bool has_z) {
   RingPlan p{};
   const int nv = N / 8;
   const size_t stage = size_t(N) * ((has_z ? 2 : 0) + (gated ? 1 : 2));
-  const size_t room = size_t(220) * 1024;
+  const size_t room = kRingRoom;
   p.vpt = (nv + kDactRingThreads - 1) / kDactRingThreads;
   p.threads = ring_threads(nv, p.vpt);
   p.rows = 1;
@@ -1343,12 +1355,12 @@ FusedBwdLayout fused_bwd_layout(int M, const qlin_weights* w) {
 template <bool GATED, bool ACC>
 cudaError_t launch_dact_ring(const RingPlan& p, unsigned grid, const DactArgs& g, cudaStream_t stream) {
   switch (p.vpt) {
-    case 1: return launch_ring(dact_ring_kernel<GATED, 1, ACC>, p, grid, stream, g);
-    case 2: return launch_ring(dact_ring_kernel<GATED, 2, ACC>, p, grid, stream, g);
-    case 3: return launch_ring(dact_ring_kernel<GATED, 3, ACC>, p, grid, stream, g);
-    case 4: return launch_ring(dact_ring_kernel<GATED, 4, ACC>, p, grid, stream, g);
-    case 5: return launch_ring(dact_ring_kernel<GATED, 5, ACC>, p, grid, stream, g);
-    default: return launch_ring(dact_ring_kernel<GATED, 6, ACC>, p, grid, stream, g);
+    case 1: return launch_ring<dact_ring_kernel<GATED, 1, ACC>>(p, grid, stream, g);
+    case 2: return launch_ring<dact_ring_kernel<GATED, 2, ACC>>(p, grid, stream, g);
+    case 3: return launch_ring<dact_ring_kernel<GATED, 3, ACC>>(p, grid, stream, g);
+    case 4: return launch_ring<dact_ring_kernel<GATED, 4, ACC>>(p, grid, stream, g);
+    case 5: return launch_ring<dact_ring_kernel<GATED, 5, ACC>>(p, grid, stream, g);
+    default: return launch_ring<dact_ring_kernel<GATED, 6, ACC>>(p, grid, stream, g);
   }
 }
 
@@ -1387,7 +1399,9 @@ qlin_status launch_dx(const qlin_weights* w, int M, const FusedBwdLayout& L, cha
   if (st != QLIN_OK) return st;
   st = make_map(&prm.tmX, dX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->K, M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != QLIN_OK) return st;
-  cudaError_t e = launch_kc(dx_pair_kernel, dim3(static_cast<unsigned>(2 * p.ncl)), dim3(DxCfg::kThreads), DxCfg::kSmem,
+  cudaError_t e = allow_smem<dx_pair_kernel>(DxCfg::kSmem);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dx_pair_kernel attribute: %s", cudaGetErrorString(e));
+  e = launch_kc(dx_pair_kernel, dim3(static_cast<unsigned>(2 * p.ncl)), dim3(DxCfg::kThreads), DxCfg::kSmem,
                             stream, 2, prm);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dx_pair_kernel launch failed: %s", cudaGetErrorString(e));
   if (p.S > 1) {
@@ -1499,19 +1513,19 @@ cudaError_t launch_norm_t(const NormFwdArgs& g, cudaStream_t stream) {
 
 template <bool ACC>
 cudaError_t launch_norm_backward_ring(const RingPlan& p, unsigned grid, const NormBwdArgs& g, cudaStream_t stream) {
-  if (p.vpt == 4) return launch_ring(norm_backward_ring_kernel<4, 1, ACC>, p, grid, stream, g);
+  if (p.vpt == 4) return launch_ring<norm_backward_ring_kernel<4, 1, ACC>>(p, grid, stream, g);
   if (p.vpt == 2)
-    return p.rows == 2 ? launch_ring(norm_backward_ring_kernel<2, 2, ACC>, p, grid, stream, g)
-                       : launch_ring(norm_backward_ring_kernel<2, 1, ACC>, p, grid, stream, g);
-  return p.rows == 4 ? launch_ring(norm_backward_ring_kernel<1, 4, ACC>, p, grid, stream, g)
-                     : launch_ring(norm_backward_ring_kernel<1, 1, ACC>, p, grid, stream, g);
+    return p.rows == 2 ? launch_ring<norm_backward_ring_kernel<2, 2, ACC>>(p, grid, stream, g)
+                       : launch_ring<norm_backward_ring_kernel<2, 1, ACC>>(p, grid, stream, g);
+  return p.rows == 4 ? launch_ring<norm_backward_ring_kernel<1, 4, ACC>>(p, grid, stream, g)
+                     : launch_ring<norm_backward_ring_kernel<1, 1, ACC>>(p, grid, stream, g);
 }
 
 cudaError_t launch_norm_forward_ring(const RingPlan& p, unsigned grid, const NormFwdArgs& g, cudaStream_t stream) {
   // only calls with more rows than persistent CTAs come here: groups are full
-  if (p.vpt == 4) return launch_ring(norm_forward_ring_kernel<4, 1>, p, grid, stream, g);
-  if (p.vpt == 2) return launch_ring(norm_forward_ring_kernel<2, 2>, p, grid, stream, g);
-  return launch_ring(norm_forward_ring_kernel<1, 4>, p, grid, stream, g);
+  if (p.vpt == 4) return launch_ring<norm_forward_ring_kernel<4, 1>>(p, grid, stream, g);
+  if (p.vpt == 2) return launch_ring<norm_forward_ring_kernel<2, 2>>(p, grid, stream, g);
+  return launch_ring<norm_forward_ring_kernel<1, 4>>(p, grid, stream, g);
 }
 
 // Partial rows of dgamma and dbeta: one per CTA of the ring kernel, else one

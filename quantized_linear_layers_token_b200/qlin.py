@@ -363,15 +363,16 @@ def _buf(t, dtype, n: int, name: str) -> int | None:
     (the stream's)."""
     if t is None or isinstance(t, int):
         return t
+    device = t.get_device()  # -1: not on a GPU
+    if t.dtype is dtype and t.is_contiguous() and t.numel() >= n and device >= 0 and device == torch._C._cuda_getDevice():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
     if t.numel() < n:
         raise ValueError(f"{name} has {t.numel()} elements, {n} are needed")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
 
 
 def qlin_forward_act_workspace(M: int, w: qlin_weights) -> int:
