@@ -41,6 +41,25 @@ struct EpiArgs {
   int act;
 };
 
+// Eight fp16 values as four fp32 pairs, and back (rounded once).
+__device__ __forceinline__ void h8_to_f2(const uint4 v, f32x2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+    f[e] = f2_pack(t.x, t.y);
+  }
+}
+__device__ __forceinline__ uint4 f2_to_h8(const f32x2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 t = f2_unpack(f[e]);
+    const __half2 h = __floats2half2_rn(t.x, t.y);
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // The arithmetic runs on fp32 pairs (one instruction for two values); the
 // exponential and the reciprocal are a special-function operation a value.
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -91,44 +110,51 @@ __device__ __forceinline__ f32x2 normal_cdf(f32x2 z, f32x2& e) {
   return f2_pack(v.x < 0.f ? q.x : 1.f - q.x, v.y < 0.f ? q.y : 1.f - q.y);
 }
 
-// act(z) of N values (N even), the choice made once.
+// act(z) of N pairs, the choice made once.
 template <int N>
-__device__ __forceinline__ void act_values(int act, float (&z)[N]) {
-  static_assert(N % 2 == 0, "values go in pairs");
-  auto put = [&](int i, f32x2 v) {
-    const float2 t = f2_unpack(v);
-    z[i] = t.x;
-    z[i + 1] = t.y;
-  };
+__device__ __forceinline__ void act_pairs(int act, f32x2 (&z)[N]) {
   switch (act) {
     case kActRelu:
 #pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];
+      for (int i = 0; i < N; ++i) {
+        const float2 v = f2_unpack(z[i]);
+        z[i] = f2_pack(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);
+      }
       break;
     case kActGelu:
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const f32x2 v = f2_pack(z[i], z[i + 1]);
+      for (int i = 0; i < N; ++i) {
         f32x2 e;
-        put(i, f2_mul(v, normal_cdf(v, e)));
+        z[i] = f2_mul(z[i], normal_cdf(z[i], e));
       }
       break;
     case kActGeluTanh:
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const f32x2 v = f2_pack(z[i], z[i + 1]);
+      for (int i = 0; i < N; ++i) {
         f32x2 z2;
-        put(i, f2_mul(v, logistic2(f2_mul(gelu_cubic(v, z2), f2_both(-kGeluTanhA * kLog2e)))));
+        z[i] = f2_mul(z[i], logistic2(f2_mul(gelu_cubic(z[i], z2), f2_both(-kGeluTanhA * kLog2e))));
       }
       break;
     case kActSilu:
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const f32x2 v = f2_pack(z[i], z[i + 1]);
-        put(i, f2_mul(v, logistic2(f2_mul(v, f2_both(-kLog2e)))));
-      }
+      for (int i = 0; i < N; ++i) z[i] = f2_mul(z[i], logistic2(f2_mul(z[i], f2_both(-kLog2e))));
       break;
     default: break;
+  }
+}
+// The same of N values, N even.
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&z)[N]) {
+  static_assert(N % 2 == 0, "values go in pairs");
+  f32x2 v[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) v[i] = f2_pack(z[2 * i], z[2 * i + 1]);
+  act_pairs<N / 2>(act, v);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 t = f2_unpack(v[i]);
+    z[2 * i] = t.x;
+    z[2 * i + 1] = t.y;
   }
 }
 

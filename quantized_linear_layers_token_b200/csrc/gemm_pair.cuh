@@ -16,8 +16,7 @@
 // the outlier channels (the Quaff term X_hat[:,O] (s_O - 1) W_O) runs
 // after the K-blocks of a tile as kind::f16 pair operations of W_O^T x U
 // (hi and lo passes) into a second accumulator; the epilogue computes
-// Y = fp16(a_m (c'_n acc + comp)) exactly as the single-CTA kernel does, or
-// goes on from there in fp32 (EPI; epilogue.cuh).
+// Y = fp16(a_m (c'_n acc + comp)) exactly as the single-CTA kernel does.
 //
 // Roles per CTA (both CTAs of a pair run all of them, the MMA only in the
 // even CTA):
@@ -97,7 +96,6 @@ struct PairArgs {
   float* ws_comp;
   unsigned* ws_cnt;   // [tiles - dp][2], zero between launches
   unsigned bnd[kMaxPairs + 1];
-  EpiArgs epi;        // fused epilogues
 };
 
 struct alignas(64) PairParams {
@@ -105,8 +103,7 @@ struct alignas(64) PairParams {
   CUtensorMap tmX;   // Xq int8 [M][K], 128 x 128 boxes, 128-byte swizzle
   CUtensorMap tmU;   // U fp16 [2M][nOp], 64 x 128 boxes, 128-byte swizzle
   CUtensorMap tmWo;  // W_O^T blocks as rows of 128 bytes: [ntn * ncs * 128][128]
-  CUtensorMap tmY;   // Y fp16 [M][N], 128 x 256 boxes (stores); gated: [M][N / 2], 64 x 256 boxes
-  CUtensorMap tmZ;   // fused epilogues with Z: fp16 [M][N], 128 x 256 boxes (stores)
+  CUtensorMap tmY;   // Y fp16 [M][N], 128 x 256 boxes (stores)
   PairArgs g;
 };
 
@@ -172,85 +169,7 @@ __device__ __forceinline__ int pair_owner(const PairArgs& g, unsigned it) {
   return lo;
 }
 
-// Fused epilogue of one tile (EPI != kEpiPlain; whole tiles only).  The
-// accumulator is single-buffered, so the tensor cores stand still while it is
-// read: each thread drains its 128 values into registers first (two products
-// and a sum each), releases it, and does the rest -- bias, activation,
-// residual, product, rounding and the stores -- under the next tile's
-// products.
-//   Z first passes through the output tile in shared memory when it is
-// kept; the gated output is 64 channels wide.  The activation is a template
-// parameter: this code is unrolled over the registers, and five activations
-// in every copy were enough to miss the instruction cache.
-template <int EPI, int ACT>
-__device__ __forceinline__ void pair_epi_tile(const PairParams& prm, unsigned char* smem_y, const float* sa,
-                                              float (&v)[8][16], int ctile, int m0, int mvalid, int grp, int nl,
-                                              bool issuer) {
-  const PairArgs& g = prm.g;
-  const EpiArgs& e = g.epi;
-  uint16_t* ys = reinterpret_cast<uint16_t*>(smem_y);
-  const int n = ctile * 128 + nl;
-  const bool in = n < g.N;
-  const float bias = e.bias && in ? __ldg(e.bias + n) : -0.f;  // adding -0 changes no value
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const int c0 = grp * 16 + c * 32;
-#pragma unroll
-    for (int q4 = 0; q4 < 4; ++q4) {
-      const float4 s4 = *reinterpret_cast<const float4*>(sa + c0 + 4 * q4);
-      v[c][4 * q4] = __fadd_rn(__fmul_rn(s4.x, v[c][4 * q4]), bias);
-      v[c][4 * q4 + 1] = __fadd_rn(__fmul_rn(s4.y, v[c][4 * q4 + 1]), bias);
-      v[c][4 * q4 + 2] = __fadd_rn(__fmul_rn(s4.z, v[c][4 * q4 + 2]), bias);
-      v[c][4 * q4 + 3] = __fadd_rn(__fmul_rn(s4.w, v[c][4 * q4 + 3]), bias);
-    }
-  }
-  if (e.Z) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) ys[(grp * 16 + c * 32 + j) * 128 + nl] = __half_as_ushort(__float2half_rn(v[c][j]));
-    fence_proxy_async_smem();
-    named_bar_sync(1, 256);
-    if (issuer) {
-      if (ctile * 128 < g.N) tma_store_2d(&prm.tmZ, ys, ctile * 128, m0);
-      bulk_commit_group();
-      bulk_wait_group_read0();
-    }
-    named_bar_sync(1, 256);
-  }
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const int c0 = grp * 16 + c * 32;
-    if (EPI == kEpiGated) {
-      const bool odd = nl & 1;
-      float h[8];
-      gated_pair<16>(ACT, v[c], odd, 0xffffffffu, h);
-      const int t0 = c0 + (odd ? 8 : 0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ys[(t0 + i) * 64 + (nl >> 1)] = __half_as_ushort(__float2half_rn(h[i]));
-    } else {
-      act_values<16>(ACT, v[c]);
-      if (e.residual) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint16_t res[8];  // a warp reads 32 neighbouring channels of one token: two full sectors
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int m = c0 + 8 * h + j;
-            res[j] = (m < mvalid && in) ? e.residual[static_cast<size_t>(m0 + m) * g.N + n] : uint16_t(0);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[c][8 * h + j] = __fadd_rn(v[c][8 * h + j], __half2float(__ushort_as_half(res[j])));
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) ys[(c0 + j) * 128 + nl] = __half_as_ushort(__float2half_rn(v[c][j]));
-    }
-  }
-}
-
-template <int FMT, int EPI, int ACT>
+template <int FMT>
 __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1) gemm_pair_kernel(const __grid_constant__ PairParams prm) {
   using C = PairCfg<FMT>;
   const PairArgs& g = prm.g;
@@ -569,59 +488,89 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1) gemm_pair_kernel(co
       const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       // partial of a split tile: this CTA's slot, [token][channel]
       const size_t pslot = part ? (static_cast<size_t>(sg.slot) * 2 + crk) * 256 * 128 : 0;
-      if constexpr (EPI != kEpiPlain) {
-        float v[8][16];
+#pragma unroll 1
+      for (int c0 = grp * 16; c0 < mvalid; c0 += 32) {
+        uint32_t acc[16], cmp[16];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int c0 = grp * 16 + c * 32;
-          uint32_t acc[16], cmp[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) { acc[j] = 0u; cmp[j] = 0u; }
-          if (ok) {
-            tmem_ld16(trow + c0, acc);
-            if (comp) tmem_ld16(trow + 256 + c0, cmp);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            v[c][j] = __fmul_rn(cn, static_cast<float>(static_cast<int32_t>(acc[j])));
-            if (comp) v[c][j] = __fadd_rn(v[c][j], __uint_as_float(cmp[j]));
-          }
+        for (int j = 0; j < 16; ++j) { acc[j] = 0u; cmp[j] = 0u; }
+        if (ok) {
+          if (has_main) tmem_ld16(trow + c0, acc);
+          if (has_comp) tmem_ld16(trow + 256 + c0, cmp);
+          tmem_ld_wait();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader) mbar_arrive(acc_empty);
-          else mbar_arrive_remote(lempty);
+        if (part) {
+          int32_t* pa = g.ws_acc + pslot + static_cast<size_t>(c0) * 128 + nl;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pa[j * 128] = static_cast<int32_t>(acc[j]);
+          if (has_comp) {  // only a range's first segment can hold a compensation: one slot per pair
+            float* pc = g.ws_comp + (static_cast<size_t>(cid) * 2 + crk) * 256 * 128 + static_cast<size_t>(c0) * 128 + nl;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pc[j * 128] = __uint_as_float(cmp[j]);
+          }
+          continue;
         }
-        pair_epi_tile<EPI, ACT>(prm, smem + C::kOffY, sa, v, ctile, m0, mvalid, grp, nl, issuer);
-        fence_proxy_async_smem();  // the output rows are read by the bulk copy next
+        float sc[16];
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          const float4 v = *reinterpret_cast<const float4*>(sa + c0 + 4 * q4);
+          sc[4 * q4] = v.x; sc[4 * q4 + 1] = v.y; sc[4 * q4 + 2] = v.z; sc[4 * q4 + 3] = v.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float v = __fmul_rn(cn, static_cast<float>(static_cast<int32_t>(acc[j])));
+          if (comp) v = __fadd_rn(v, __uint_as_float(cmp[j]));
+          ys[(c0 + j) * 128 + nl] = __half_as_ushort(__float2half_rn(__fmul_rn(sc[j], v)));
+        }
+        if (g.acc_debug && n < g.N)
+          for (int j = 0; j < 16; ++j)
+            if (c0 + j < mvalid) g.acc_debug[static_cast<size_t>(m0 + c0 + j) * g.N + n] = static_cast<int32_t>(acc[j]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(acc_empty);
+        else mbar_arrive_remote(lempty);
+      }
+      if (part) {
+        // Count this CTA's steps of the split tile (CTA barrier, then one
+        // thread's release fence and atomic: the release covers every
+        // epilogue thread's partial stores); the range whose steps complete
+        // the tile sums every contributor's partial and writes the output.
         named_bar_sync(1, 256);
-        if (issuer && ctile * 128 < g.N) {
-          tma_store_2d(&prm.tmY, ys, ctile * (EPI == kEpiGated ? 64 : 128), m0);
-          bulk_commit_group();
+        if (ep == 0 && lane == 0) {
+          fence_acq_rel_gpu();
+          const unsigned add = static_cast<unsigned>(sg.r1 - sg.r0);
+          const unsigned old = atom_add_relaxed_gpu(&g.ws_cnt[sg.sk * 2 + crk], add);
+          const bool last = old + add == static_cast<unsigned>(g.T);
+          if (last) fence_acq_rel_gpu();  // acquire the other contributors' partials
+          *fin_flag = last ? 1 : 0;
         }
-      } else {
+        named_bar_sync(1, 256);
+        if (!*fin_flag) continue;
+        const unsigned ts = static_cast<unsigned>(sg.sk) * static_cast<unsigned>(g.T);
+        const int c_lo = pair_owner(g, ts);
+        const int c_hi = pair_owner(g, ts + static_cast<unsigned>(g.T) - 1u);
 #pragma unroll 1
         for (int c0 = grp * 16; c0 < mvalid; c0 += 32) {
-          uint32_t acc[16], cmp[16];
+          int32_t sum[16];
+          float cp[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) { acc[j] = 0u; cmp[j] = 0u; }
-          if (ok) {
-            if (has_main) tmem_ld16(trow + c0, acc);
-            if (has_comp) tmem_ld16(trow + 256 + c0, cmp);
-            tmem_ld_wait();
+          for (int j = 0; j < 16; ++j) { sum[j] = 0; cp[j] = 0.f; }
+          for (int c = c_lo; c <= c_hi; ++c) {
+            if (g.bnd[c] == g.bnd[c + 1]) continue;  // an empty range
+            const int slot = 2 * c + (g.bnd[c] < ts ? 1 : 0);
+            const int32_t* src = g.ws_acc + (static_cast<size_t>(slot) * 2 + crk) * 256 * 128 + static_cast<size_t>(c0) * 128 + nl;
+            int32_t v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __ldcg(src + j * 128);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[j] += v[j];
           }
-          if (part) {
-            int32_t* pa = g.ws_acc + pslot + static_cast<size_t>(c0) * 128 + nl;
+          if (comp) {
+            // the range holding the tile's last step holds its whole compensation
+            const float* src = g.ws_comp + (static_cast<size_t>(c_hi) * 2 + crk) * 256 * 128 + static_cast<size_t>(c0) * 128 + nl;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) pa[j * 128] = static_cast<int32_t>(acc[j]);
-            if (has_comp) {  // only a range's first segment can hold a compensation: one slot per pair
-              float* pc = g.ws_comp + (static_cast<size_t>(cid) * 2 + crk) * 256 * 128 + static_cast<size_t>(c0) * 128 + nl;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) pc[j * 128] = __uint_as_float(cmp[j]);
-            }
-            continue;
+            for (int j = 0; j < 16; ++j) cp[j] = __ldcg(src + j * 128);
           }
           float sc[16];
 #pragma unroll
@@ -631,85 +580,21 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1) gemm_pair_kernel(co
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float v = __fmul_rn(cn, static_cast<float>(static_cast<int32_t>(acc[j])));
-            if (comp) v = __fadd_rn(v, __uint_as_float(cmp[j]));
+            float v = __fmul_rn(cn, static_cast<float>(sum[j]));
+            if (comp) v = __fadd_rn(v, cp[j]);
             ys[(c0 + j) * 128 + nl] = __half_as_ushort(__float2half_rn(__fmul_rn(sc[j], v)));
           }
           if (g.acc_debug && n < g.N)
             for (int j = 0; j < 16; ++j)
-              if (c0 + j < mvalid) g.acc_debug[static_cast<size_t>(m0 + c0 + j) * g.N + n] = static_cast<int32_t>(acc[j]);
+              if (c0 + j < mvalid) g.acc_debug[static_cast<size_t>(m0 + c0 + j) * g.N + n] = sum[j];
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader) mbar_arrive(acc_empty);
-          else mbar_arrive_remote(lempty);
-        }
-        if (part) {
-          // Count this CTA's steps of the split tile (CTA barrier, then one
-          // thread's release fence and atomic: the release covers every
-          // epilogue thread's partial stores); the range whose steps complete
-          // the tile sums every contributor's partial and writes the output.
-          named_bar_sync(1, 256);
-          if (ep == 0 && lane == 0) {
-            fence_acq_rel_gpu();
-            const unsigned add = static_cast<unsigned>(sg.r1 - sg.r0);
-            const unsigned old = atom_add_relaxed_gpu(&g.ws_cnt[sg.sk * 2 + crk], add);
-            const bool last = old + add == static_cast<unsigned>(g.T);
-            if (last) fence_acq_rel_gpu();  // acquire the other contributors' partials
-            *fin_flag = last ? 1 : 0;
-          }
-          named_bar_sync(1, 256);
-          if (!*fin_flag) continue;
-          const unsigned ts = static_cast<unsigned>(sg.sk) * static_cast<unsigned>(g.T);
-          const int c_lo = pair_owner(g, ts);
-          const int c_hi = pair_owner(g, ts + static_cast<unsigned>(g.T) - 1u);
-#pragma unroll 1
-          for (int c0 = grp * 16; c0 < mvalid; c0 += 32) {
-            int32_t sum[16];
-            float cp[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) { sum[j] = 0; cp[j] = 0.f; }
-            for (int c = c_lo; c <= c_hi; ++c) {
-              if (g.bnd[c] == g.bnd[c + 1]) continue;  // an empty range
-              const int slot = 2 * c + (g.bnd[c] < ts ? 1 : 0);
-              const int32_t* src = g.ws_acc + (static_cast<size_t>(slot) * 2 + crk) * 256 * 128 + static_cast<size_t>(c0) * 128 + nl;
-              int32_t v[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = __ldcg(src + j * 128);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) sum[j] += v[j];
-            }
-            if (comp) {
-              // the range holding the tile's last step holds its whole compensation
-              const float* src = g.ws_comp + (static_cast<size_t>(c_hi) * 2 + crk) * 256 * 128 + static_cast<size_t>(c0) * 128 + nl;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) cp[j] = __ldcg(src + j * 128);
-            }
-            float sc[16];
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              const float4 v = *reinterpret_cast<const float4*>(sa + c0 + 4 * q4);
-              sc[4 * q4] = v.x; sc[4 * q4 + 1] = v.y; sc[4 * q4 + 2] = v.z; sc[4 * q4 + 3] = v.w;
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float v = __fmul_rn(cn, static_cast<float>(sum[j]));
-              if (comp) v = __fadd_rn(v, cp[j]);
-              ys[(c0 + j) * 128 + nl] = __half_as_ushort(__float2half_rn(__fmul_rn(sc[j], v)));
-            }
-            if (g.acc_debug && n < g.N)
-              for (int j = 0; j < 16; ++j)
-                if (c0 + j < mvalid) g.acc_debug[static_cast<size_t>(m0 + c0 + j) * g.N + n] = sum[j];
-          }
-          if (ep == 0 && lane == 0) g.ws_cnt[sg.sk * 2 + crk] = 0u;  // zero for the next launch
-        }
-        fence_proxy_async_smem();  // the output rows are read by the bulk copy next
-        named_bar_sync(1, 256);
-        if (issuer && ctile * 128 < g.N) {
-          tma_store_2d(&prm.tmY, ys, ctile * 128, m0);
-          bulk_commit_group();
-        }
+        if (ep == 0 && lane == 0) g.ws_cnt[sg.sk * 2 + crk] = 0u;  // zero for the next launch
+      }
+      fence_proxy_async_smem();  // the output rows are read by the bulk copy next
+      named_bar_sync(1, 256);
+      if (issuer && ctile * 128 < g.N) {
+        tma_store_2d(&prm.tmY, ys, ctile * 128, m0);
+        bulk_commit_group();
       }
     }
     if (issuer) bulk_wait_group_all();

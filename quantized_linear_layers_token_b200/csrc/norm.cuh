@@ -73,25 +73,6 @@ __device__ __forceinline__ void load_f8(const float* p, float (&f)[8]) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// The same eight values as four fp32 pairs.
-__device__ __forceinline__ void h8_to_f2(const uint4 v, f32x2 (&f)[4]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-    f[e] = f2_pack(t.x, t.y);
-  }
-}
-__device__ __forceinline__ uint4 f2_to_h8(const f32x2 (&f)[4]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 t = f2_unpack(f[e]);
-    const __half2 h = __floats2half2_rn(t.x, t.y);
-    w[e] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 __device__ __forceinline__ void load_f2x4(const float* p, f32x2 (&f)[4]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);

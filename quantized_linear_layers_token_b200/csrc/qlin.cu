@@ -15,6 +15,7 @@
 #include "qlin.h"
 #include "act_quant.cuh"
 #include "gemm.cuh"
+#include "gemm_fused.cuh"
 #include "gemm_pair.cuh"
 #include "backward.cuh"
 #include "dact.cuh"
@@ -262,7 +263,7 @@ struct GemmPlan {
 };
 
 bool use_pair(const GemmPlan& p, const qlin_weights* w);
-template <int FMT, int EPI = kEpiPlain, int ACT = kActNone>
+template <int FMT>
 int pair_max_clusters();
 
 // Work split of a launch on CTA pairs over `tiles` tiles of T steps (the
@@ -561,12 +562,12 @@ qlin_status launch_gemm_epi(int epi, int bt, GemmParams<1>& prm, cudaStream_t st
 }
 
 // ---------------------------------------------------------------- CTA-pair GEMM (many tokens)
-template <int FMT, int EPI, int ACT>
+template <int FMT>
 int pair_max_clusters() {
   static int n = -1;
   static std::once_flag once;
   std::call_once(once, [] {
-    if (cudaFuncSetAttribute(gemm_pair_kernel<FMT, EPI, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(gemm_pair_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              PairCfg<FMT>::kSmem) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
@@ -584,7 +585,7 @@ int pair_max_clusters() {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int c = 0;
-    if (cudaOccupancyMaxActiveClusters(&c, gemm_pair_kernel<FMT, EPI, ACT>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&c, gemm_pair_kernel<FMT>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       c = 0;
     }
@@ -610,10 +611,9 @@ bool use_pair(const GemmPlan& p, const qlin_weights* w) {
 // FMT = kFmtW8: INT8 weight rows by TMA from `codes8` (the INT8 format, or
 // INT4 widened ahead); kFmtW4PC / kFmtW4G128: the layer's packed INT4 codes,
 // converted inside the kernel.
-template <int FMT, int EPI = kEpiPlain, int ACT = kActNone>
+template <int FMT>
 qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
-                             int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream,
-                             const EpiArgs* epi = nullptr) {
+                             int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream) {
   PairParams prm;
   memset(&prm, 0, sizeof(prm));
   PairArgs& g = prm.g;
@@ -637,7 +637,7 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
   g.tiles_m = q.tiles_m;
   g.tiles = g.tiles_n2 * g.tiles_m;
   const double x_bytes = static_cast<double>(M) * w->K;
-  const int maxc = pair_max_clusters<FMT, EPI, ACT>();
+  const int maxc = pair_max_clusters<FMT>();
   if (maxc < 1) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel: no 2-CTA cluster fits");
   int gm = static_cast<int>(std::lround(std::sqrt(static_cast<double>(maxc) * 256.0 / 256.0)));
   if (x_bytes <= 48.0 * 1024 * 1024) gm = g.tiles_m;
@@ -665,39 +665,81 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
                   static_cast<uint64_t>(q.tiles_n) * q.ncs * 128, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != QLIN_OK) return st;
   }
-  constexpr int kYDiv = EPI == kEpiGated ? 2 : 1;  // gated: one output channel per pair
-  st = make_map(&prm.tmY, Y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N / kYDiv, M, 128 / kYDiv, 256,
-                CU_TENSOR_MAP_SWIZZLE_NONE);
+  st = make_map(&prm.tmY, Y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N, M, 128, 256, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (st != QLIN_OK) return st;
-  if (EPI != kEpiPlain) {
-    g.epi = *epi;
-    if (epi->Z) {
-      st = make_map(&prm.tmZ, epi->Z, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N, M, 128, 256, CU_TENSOR_MAP_SWIZZLE_NONE);
-      if (st != QLIN_OK) return st;
-    }
-  }
-  cudaError_t e = allow_smem<gemm_pair_kernel<FMT, EPI, ACT>>(PairCfg<FMT>::kSmem);
+  cudaError_t e = allow_smem<gemm_pair_kernel<FMT>>(PairCfg<FMT>::kSmem);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel attribute: %s", cudaGetErrorString(e));
-  e = launch_kc(gemm_pair_kernel<FMT, EPI, ACT>, dim3(static_cast<unsigned>(2 * g.ncl)),
+  e = launch_kc(gemm_pair_kernel<FMT>, dim3(static_cast<unsigned>(2 * g.ncl)),
                             dim3(PairCfg<FMT>::kThreads), PairCfg<FMT>::kSmem, stream, 2, prm);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_pair_kernel launch failed: %s", cudaGetErrorString(e));
   return QLIN_OK;
 }
 
-// A fused epilogue on CTA pairs, its activation chosen at run time.
+// A fused layer on CTA pairs.  INT8 weight rows from `codes8` (the INT8
+// format, or INT4 widened ahead).
+template <int EPI, int ACT>
+qlin_status launch_fused_t(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
+                           char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream, const EpiArgs& epi) {
+  FusedPairParams prm;
+  memset(&prm, 0, sizeof(prm));
+  FusedPairArgs& g = prm.g;
+  const GemmProb& q = p.pr[0];
+  const int M = q.M;
+  g.cscale = w->chan_scale;
+  g.cmul = cmul;
+  g.a = a;
+  g.M = M;
+  g.N = w->N;
+  g.nO = w->n_outlier;
+  g.kb = q.kb;
+  g.ntn = q.tiles_n;
+  g.ncs = q.ncs;
+  g.tiles_n2 = (q.tiles_n + 1) / 2;
+  g.tiles_m = q.tiles_m;
+  g.tiles = g.tiles_n2 * g.tiles_m;
+  g.ncl = p.pair_ncl;
+  g.epi = epi;
+  int gm = static_cast<int>(std::lround(std::sqrt(static_cast<double>(g.ncl))));
+  if (static_cast<double>(M) * w->K <= 48.0 * 1024 * 1024) gm = g.tiles_m;
+  g.gm = gm < 1 ? 1 : (gm > g.tiles_m ? g.tiles_m : gm);
+  qlin_status st = make_map(&prm.tmA, codes8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128,
+                            static_cast<uint64_t>(q.tiles_n) * q.kb * 128, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (st != QLIN_OK) return st;
+  st = make_map(&prm.tmX, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->K, M, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != QLIN_OK) return st;
+  if (w->n_outlier > 0) {
+    st = make_map(&prm.tmU, gws + p.u_off[0], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->n_outlier_pad,
+                  2 * static_cast<uint64_t>(M), 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != QLIN_OK) return st;
+    st = make_map(&prm.tmWo, w->W_Ot, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128,
+                  static_cast<uint64_t>(q.tiles_n) * q.ncs * 128, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (st != QLIN_OK) return st;
+  }
+  const int F = EPI == kEpiGated ? w->N / 2 : w->N;
+  st = make_map(&prm.tmY, Y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, F, M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != QLIN_OK) return st;
+  if (epi.Z) {
+    st = make_map(&prm.tmZ, epi.Z, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N, M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != QLIN_OK) return st;
+  }
+  constexpr auto kern = gemm_fused_kernel<EPI, ACT>;
+  cudaError_t e = allow_smem<kern>(FusedPairCfg::kSmem);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_fused_kernel attribute: %s", cudaGetErrorString(e));
+  e = launch_kc(kern, dim3(static_cast<unsigned>(2 * g.ncl)), dim3(FusedPairCfg::kThreads), FusedPairCfg::kSmem, stream,
+                2, prm);
+  if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_fused_kernel launch failed: %s", cudaGetErrorString(e));
+  return QLIN_OK;
+}
+
 template <int EPI>
-qlin_status launch_pair_act(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
-                            char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream, const EpiArgs* epi) {
-  switch (epi->act) {
-    case kActRelu:
-      return launch_gemm_pair<kFmtW8, EPI, kActRelu>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
-    case kActGelu:
-      return launch_gemm_pair<kFmtW8, EPI, kActGelu>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
-    case kActGeluTanh:
-      return launch_gemm_pair<kFmtW8, EPI, kActGeluTanh>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
-    case kActSilu:
-      return launch_gemm_pair<kFmtW8, EPI, kActSilu>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
-    default: return launch_gemm_pair<kFmtW8, EPI, kActNone>(p, w, Xq, a, Y, nullptr, gws, codes8, cmul, stream, epi);
+qlin_status launch_fused_act(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
+                             char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream, const EpiArgs& epi) {
+  switch (epi.act) {
+    case kActRelu: return launch_fused_t<EPI, kActRelu>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
+    case kActGelu: return launch_fused_t<EPI, kActGelu>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
+    case kActGeluTanh: return launch_fused_t<EPI, kActGeluTanh>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
+    case kActSilu: return launch_fused_t<EPI, kActSilu>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
+    default: return launch_fused_t<EPI, kActNone>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
   }
 }
 
@@ -705,8 +747,8 @@ qlin_status launch_pair_act(const GemmPlan& p, const qlin_weights* w, const int8
 qlin_status launch_pair_w8(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
                            int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream,
                            const EpiArgs* epi, int variant) {
-  if (variant == kEpiGated) return launch_pair_act<kEpiGated>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
-  if (variant == kEpiAct) return launch_pair_act<kEpiAct>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
+  if (variant == kEpiGated) return launch_fused_act<kEpiGated>(p, w, Xq, a, Y, gws, codes8, cmul, stream, *epi);
+  if (variant == kEpiAct) return launch_fused_act<kEpiAct>(p, w, Xq, a, Y, gws, codes8, cmul, stream, *epi);
   return launch_gemm_pair<kFmtW8>(p, w, Xq, a, Y, acc_debug, gws, codes8, cmul, stream);
 }
 
