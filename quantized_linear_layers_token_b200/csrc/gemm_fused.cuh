@@ -46,6 +46,7 @@ struct alignas(64) FusedPairParams {
   CUtensorMap tmWo;  // W_O^T blocks as rows of 128 bytes
   CUtensorMap tmY;   // Y fp16 [M][N], gated [M][N / 2]: 64 x 128 boxes, 128-byte swizzle (stores)
   CUtensorMap tmZ;   // Z fp16 [M][N], the same boxes
+  CUtensorMap tmR;   // residual fp16 [M][N], the same boxes (loads)
   FusedPairArgs g;
 };
 
@@ -90,7 +91,8 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
   uint64_t* main_empty = main_full + 2;                              // [2] the even CTA's
   uint64_t* comp_full = main_empty + 2;                              // each CTA's own
   uint64_t* comp_empty = comp_full + 1;                              // the even CTA's
-  uint64_t* mma_done = comp_empty + 1;
+  uint64_t* res_full = comp_empty + 1;                               // [2] residual boxes of each epilogue group
+  uint64_t* mma_done = res_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5;
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
     for (int b = 0; b < 2; ++b) {
       mbar_init(&main_full[b], 1);
       mbar_init(&main_empty[b], 2 * C::kEpiWarps);
+      mbar_init(&res_full[b], 1);
     }
     mbar_init(comp_full, 1);
     mbar_init(comp_empty, 2 * C::kEpiWarps);
@@ -268,9 +271,39 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
       const int n0 = tn2 * 256 + grp * 128;  // the group's first channel
       const int m0 = tm * 256 + crk * 128;
       const int m = m0 + row;
+      // the group's boxes leave through TMA; `store` hands them over once every
+      // thread of the group has written
+      auto take_boxes = [&] {
+        if (issuer) bulk_wait_group_read0();
+        named_bar_sync(gbar, 128);
+      };
+      // the issuer has taken the boxes: the residual on its way into them
+      auto load_residual = [&] {
+        int n = 0;
+        for (int b = 0; b < 2; ++b) n += n0 + 64 * b < g.N && m0 < g.M ? 1 : 0;
+        mbar_arrive_expect_tx(&res_full[grp], static_cast<uint32_t>(n) * 16384u);
+        for (int b = 0; b < n; ++b)
+          tma_load_2d(smem + C::kOffY + (grp * 2 + b) * 16384, &prm.tmR, &res_full[grp], n0 + 64 * b, m0);
+      };
+      auto store_boxes = [&](const CUtensorMap* map, int boxes, int width) {
+        fence_proxy_async_smem();
+        named_bar_sync(gbar, 128);
+        if (issuer) {
+          const int x0 = (tn2 * 2 + grp) * 64 * boxes;
+          for (int b = 0; b < boxes; ++b)
+            if (x0 + 64 * b < width && m0 < g.M)
+              tma_store_2d(map, smem + C::kOffY + (grp * 2 + b) * 16384, x0 + 64 * b, m0);
+          bulk_commit_group();
+        }
+      };
       named_bar_sync(gbar, 128);  // the previous tile's factors have been used
       sc[gt] = n0 + gt < g.N ? __fmul_rn(g.cscale[n0 + gt], g.cmul) : 0.f;
       const float am = m < g.M ? g.a[m] : 0.f;
+      const bool residual = EPI == kEpiAct && e.residual;
+      if (residual && !e.Z && issuer) {  // (with Z the boxes hold that first)
+        bulk_wait_group_read0();
+        load_residual();
+      }
       named_bar_sync(gbar, 128);
       if (ok) ok = mbar_wait(&main_full[buf], static_cast<uint32_t>(use) & 1u, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
@@ -331,24 +364,7 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
           }
         }
       }
-      // the group's boxes leave through TMA; `store` hands them over once every
-      // thread of the group has written
-      auto take_boxes = [&] {
-        if (issuer) bulk_wait_group_read0();
-        named_bar_sync(gbar, 128);
-      };
-      auto store_boxes = [&](const CUtensorMap* map, int boxes, int width) {
-        fence_proxy_async_smem();
-        named_bar_sync(gbar, 128);
-        if (issuer) {
-          const int x0 = (tn2 * 2 + grp) * 64 * boxes;
-          for (int b = 0; b < boxes; ++b)
-            if (x0 + 64 * b < width && m0 < g.M)
-              tma_store_2d(map, smem + C::kOffY + (grp * 2 + b) * 16384, x0 + 64 * b, m0);
-          bulk_commit_group();
-        }
-      };
-      take_boxes();
+      if (!residual || e.Z) take_boxes();
       if (e.Z) {
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -356,7 +372,15 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
           *reinterpret_cast<uint4*>(box0 + (q >> 3) * 16384 + (((q & 7) ^ sw) << 4)) = f2_to_h8(o);
         }
         store_boxes(&prm.tmZ, 2, g.N);
-        take_boxes();
+        if (residual && issuer) {
+          bulk_wait_group_read0();
+          load_residual();
+        }
+        if (!residual) take_boxes();
+      }
+      if (residual) {
+        if (ok) ok = mbar_wait(&res_full[grp], static_cast<uint32_t>(ti) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (EPI == kEpiGated) {
 #pragma unroll
@@ -374,23 +398,27 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
           *reinterpret_cast<uint4*>(box0 + ((q ^ sw) << 4)) = f2_to_h8(h);
         }
       } else {
-        const uint16_t* res = e.residual + static_cast<size_t>(m) * g.N + n0;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
+          uint4* at = reinterpret_cast<uint4*>(box0 + (q >> 3) * 16384 + (((q & 7) ^ sw) << 4));
           f32x2 o[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
           act_pairs<4>(ACT, o);
-          if (e.residual) {
+          if (residual) {
             f32x2 x[4];
-            h8_to_f2(m < g.M && n0 + 8 * q < g.N ? *reinterpret_cast<const uint4*>(res + 8 * q) : make_uint4(0u, 0u, 0u, 0u), x);
+            h8_to_f2(*at, x);
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[j] = f2_add(o[j], x[j]);
           }
-          *reinterpret_cast<uint4*>(box0 + (q >> 3) * 16384 + (((q & 7) ^ sw) << 4)) = f2_to_h8(o);
+          *at = f2_to_h8(o);
         }
       }
       store_boxes(&prm.tmY, kOut, F);
     }
-    if (issuer) bulk_wait_group_all();
+    if (issuer) {
+      bulk_wait_group_all();
+      // a residual box still on its way (only after a wait gave up) lands before the CTA leaves
+      if (*abort_flag && EPI == kEpiAct && e.residual) drain_ring(&res_full[grp], 1, ti);
+    }
   }
   tc_fence_before();
   __syncthreads();

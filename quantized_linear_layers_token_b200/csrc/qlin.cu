@@ -722,6 +722,11 @@ qlin_status launch_fused_t(const GemmPlan& p, const qlin_weights* w, const int8_
     st = make_map(&prm.tmZ, epi.Z, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N, M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != QLIN_OK) return st;
   }
+  if (epi.residual) {
+    st = make_map(&prm.tmR, epi.residual, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->N, M, 64, 128,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != QLIN_OK) return st;
+  }
   constexpr auto kern = gemm_fused_kernel<EPI, ACT>;
   cudaError_t e = allow_smem<kern>(FusedPairCfg::kSmem);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "gemm_fused_kernel attribute: %s", cudaGetErrorString(e));
@@ -1211,7 +1216,7 @@ qlin_status forward_fused(const uint16_t* X, int32_t M, const qlin_weights* w, f
 int column_groups(int M, int nv) {
   const int gx = (nv + 127) / 128;
   const int want = (4 * sm_count() + gx - 1) / gx;
-  const int most = (M + 7) / 8;
+  const int most = (M - 1) / 8 + 1;
   const int G = want < most ? want : most;
   return G < 1 ? 1 : (G > 65535 ? 65535 : G);
 }
@@ -1329,7 +1334,7 @@ RingPlan norm_ring_plan(int M, int K, int arrays, bool backward) {
     two.ctas = ring_ctas(two, 512);
     if (two.ctas > p.ctas) p = two;
     // one row at a time where groups would leave SMs idle or do not fit
-    if (p.rows == 1 || (p.ctas > 0 && (M + p.rows - 1) / p.rows >= sm_count())) break;
+    if (p.rows == 1 || (p.ctas > 0 && (M - 1) / p.rows + 1 >= sm_count())) break;
   }
   return p;
 }
@@ -1342,8 +1347,8 @@ cudaError_t launch_ring(const RingPlan& p, unsigned grid, cudaStream_t stream, c
 }
 
 unsigned ring_grid(const RingPlan& p, int M) {
-  if (p.ctas == 0) return 0;
-  const int groups = (M + p.rows - 1) / p.rows, most = sm_count() * p.ctas;
+  if (p.ctas == 0 || M < 1) return 0;
+  const int groups = (M - 1) / p.rows + 1, most = sm_count() * p.ctas;
   return static_cast<unsigned>(groups < most ? groups : most);
 }
 

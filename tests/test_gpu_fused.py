@@ -187,6 +187,20 @@ def test_residual_in_place(q, oracle, M):
     assert torch.equal(want, got)
 
 
+@pytest.mark.parametrize("nO", [0, 9])
+@pytest.mark.parametrize("N", [16, 80, 144, 272, 2064])
+def test_many_tiles_with_residual(q, oracle, N, nO):
+    """Several tiles per pair of CTAs, ragged at both ends, with and without
+    the kept pre-activation; the residual replaced in place."""
+    for M in (400, 2600 if N < 2000 else 2900):
+        L = Layer(q, oracle, synth.W8_PERCHANNEL, M, 128, N, nO)
+        want = check_forward(L, "silu", keep_z=True)
+        assert torch.equal(want, check_forward(L, "silu"))
+        Y = cuda(L.res)
+        assert torch.equal(want, L.forward("silu", Y=Y, res=Y)[0])
+        check_forward(Layer(q, oracle, synth.W8_PERCHANNEL, M, 128, N, nO, gated=True), "gelu", keep_z=True)
+
+
 def test_rows_and_columns_outside_are_left(q, oracle):
     """Nothing behind the last token or the last channel's row is written."""
     for M in (1, 17, 70, 300):
@@ -240,9 +254,10 @@ def check_backward(L, act, seed=1, dy_std=2.0 ** -7, with_dbias=True, z=None):
     db = torch.full((L.N,), float("nan"), device="cuda") if with_dbias else None
     size = q.qlin_backward_gated_workspace if L.gated else q.qlin_backward_act_workspace
     ws, n = ws_for(q, size(L.M, L.w))
+    ws.fill_(255)  # no zero-fill needed
     call = q.qlin_backward_gated if L.gated else q.qlin_backward_act
     got = []
-    for _ in range(2):  # the second call finds the workspace as the first left it
+    for _ in range(2):
         call(L.w, dYd, Zd, L.M, sd, dX, db, ws, n, act=ref.ACTS.index(act))
         got.append((dX.clone(), None if db is None else db.clone()))
     q.qlin_poll_device_status()
