@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(DxCfg::kThreads, 1) dx_pair_kernel(const __gri
       }
       // every stage this CTA filled has been consumed by the pair's MMAs (so
       // its copies have landed) before the CTA can leave
+      const uint64_t t0 = globaltimer_ns();  // one limit for the whole ring
       for (int t = gi - 1; t >= 0 && t >= gi - S; --t) {
-        const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait_sleep(&empty[t % S], static_cast<uint32_t>(t / S) & 1u, 1000000u) &&
                globaltimer_ns() - t0 < QLIN_DRAIN_NS) {
         }
