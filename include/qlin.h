@@ -324,8 +324,9 @@ typedef enum {
  *   Z[m][n] = a_m * ( c'_n * acc[m][n] + comp[m][n] ) + bias[n]
  *   Y[m][n] = fp16( act(Z[m][n]) + residual[m][n] )
  * with a, acc and comp of qlin_forward; everything after acc is fp32 and Y
- * is rounded once.  Without bias, activation and residual Y is qlin_forward's,
- * bit for bit.
+ * is rounded once.  Without bias, activation and residual Y is qlin_forward's
+ * up to the order in which comp's products are summed (the two may split the
+ * work differently; acc is exact in both).
  *   act       qlin_act.
  *   bias      device fp32 [N], or NULL.
  *   residual  device fp16 [M][N], or NULL.  Y may be the same buffer (the

@@ -55,26 +55,36 @@ class GatedFeedForward:
         self.s_down = torch.ones(down.n_outlier, device=dev)
         self._ws = {}        # name -> (workspace, token count) of the last call
         self._captured = {}  # (name, token count) -> workspace of captured calls
+        self._of_graphs = []  # workspaces first made under a capture, one call's each
 
     def _workspace(self, name: str, nbytes: int, M: int):
         """A zero-filled buffer that belongs to one token count: what a call
         leaves zero lies elsewhere at another count."""
         ws = self._captured.get((name, M))
         if ws is None:
+            capturing = torch.cuda.is_current_stream_capturing()
             ws, n = self._ws.get(name, (None, -1))
             if n != M or ws.numel() < nbytes:
                 ws = qlin.empty_workspace(nbytes, device=self.gated.buffer.device)
+                if capturing:  # zeroed by the graph that is being captured, when it is replayed: for no other call
+                    self._of_graphs.append(ws)
+                    return ws, nbytes
                 self._ws[name] = (ws, M)
-            if torch.cuda.is_current_stream_capturing():
+            if capturing:
                 self._captured[name, M] = ws
         return ws, nbytes
+
+    def _rows(self, t: torch.Tensor, name: str) -> int:
+        if t.dim() != 2 or t.shape[1] != self.D:
+            raise ValueError(f"{name} must be [M][{self.D}], got {tuple(t.shape)}")
+        return t.shape[0]
 
     def _half(self, *shape):
         return torch.empty(shape, dtype=torch.float16, device=self.gated.buffer.device)
 
     def forward(self, x: torch.Tensor, training: bool = False):
         """y [M][D] of x fp16 [M][D]; with `training`, (y, Saved)."""
-        M = x.shape[0]
+        M = self._rows(x, "x")
         n, h, y = self._half(M, self.D), self._half(M, self.F), self._half(M, self.D)
         z = self._half(M, 2 * self.F) if training else None
         f32 = dict(dtype=torch.float32, device=n.device)
@@ -94,7 +104,9 @@ class GatedFeedForward:
     def backward(self, saved: Saved, dy: torch.Tensor) -> dict:
         """Gradients of x and of the trainable vectors (None where there is
         no such vector): dx, dgamma, dbeta, dbias_gated, dbias_down."""
-        M = dy.shape[0]
+        M = self._rows(dy, "dy")
+        if M != saved.x.shape[0]:
+            raise ValueError(f"dy has {M} rows, the forward had {saved.x.shape[0]}")
         dev = self.gated.buffer.device
         dh, dn, dx = self._half(M, self.F), self._half(M, self.D), self._half(M, self.D)
 

@@ -179,3 +179,43 @@ def test_block_refuses_layers_that_do_not_fit(q):
     gated = q.PackedLayer(256, 512, synth.W8_PERCHANNEL, 0)
     with pytest.raises(ValueError):
         GatedFeedForward(gated, q.PackedLayer(512, 256, synth.W8_PERCHANNEL, 0), torch.ones(256, device="cuda"))
+
+
+def test_block_captured_at_a_new_token_count(q, oracle):
+    """Captured without an eager call of that token count before, then called
+    eagerly and replayed, in either order, and captured twice: one result."""
+    make = lambda: Block(q, oracle, synth.W4_G128, 256, 384, 5, q.QLIN_NORM_RMS, bias=False)  # noqa: E731
+    x = make().c(make().x(300, 256))
+    want = make().ffn.forward(x)
+    for eager_first in (True, False):
+        b = make()
+        b.ffn.forward(x[:7])
+        graphs, outs = [], []
+        junk = torch.empty(1 << 26, dtype=torch.uint8, device="cuda").fill_(255)
+        del junk
+        for _ in range(2):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                outs.append(b.ffn.forward(x))
+        if eager_first:
+            assert torch.equal(b.ffn.forward(x), want)
+        for k in (1, 0, 1):
+            outs[k].zero_()
+            graphs[k].replay()
+            assert torch.equal(outs[k], want), k
+        assert torch.equal(b.ffn.forward(x), want)
+    q.qlin_poll_device_status()
+
+
+def test_block_refuses_other_shapes(q, oracle):
+    """A padded batch, another width, or gradients of another token count."""
+    b = Block(q, oracle, synth.W8_PERCHANNEL, 256, 384, 0, q.QLIN_NORM_RMS, bias=False)
+    x = b.c(b.x(6, 256))
+    for bad in (x.view(2, 3, 256), x.view(3, 512), x.view(12, 128), x.t(), x.float(), x.cpu()):
+        with pytest.raises(ValueError):
+            b.ffn.forward(bad)
+    y, saved = b.ffn.forward(x, training=True)
+    for bad in (y[:5], y.view(2, 3, 256), y.float()):
+        with pytest.raises(ValueError):
+            b.ffn.backward(saved, bad)
+    assert b.ffn.forward(x[:0]).shape == (0, 256)
