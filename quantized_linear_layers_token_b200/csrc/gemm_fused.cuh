@@ -15,7 +15,12 @@
 // under the next tile's products.  Without outliers two accumulators alternate
 // and nothing waits.  With outliers the second half of tensor memory holds the
 // compensation: it is committed and given back apart, so the main accumulator
-// is drained under the compensation's products.
+// is drained under the compensation's products.  Measured: INT8 2048 -> 8192
+// at 4736 tokens, GELU, no outliers, 72 us (2200 TOPS) against 94 with one
+// accumulator and the channels as the product's rows.
+//
+// The tiles of a short last wave run as halves of 128 channels, each left to
+// the epilogue group of its channels.
 //
 // Warps 0..3 control (0 loads, 1 tensor memory and products), warps 4..11
 // epilogue in two groups of four, group g taking channels 128 g .. +127 of the
@@ -35,15 +40,18 @@ struct FusedPairArgs {
   int kb;   // 128-wide K-blocks
   int ntn;  // 128-channel tiles of the weights
   int ncs;  // 64-wide outlier slices
-  int tiles_n2, tiles_m, gm, tiles, ncl;
+  int tiles_n2, tiles_m, gm, ncl;
+  int whole, units;  // tiles 0 .. whole - 1, then the other tiles' halves
   EpiArgs epi;
 };
 
 struct alignas(64) FusedPairParams {
   CUtensorMap tmA;   // weight blocks as rows of 128 bytes
+  CUtensorMap tmAh;  // the same, boxes of half a block
   CUtensorMap tmX;   // Xq int8 [M][K], 128 x 128 boxes, 128-byte swizzle
   CUtensorMap tmU;   // U fp16 [2M][nOp], 64 x 128 boxes, 128-byte swizzle
   CUtensorMap tmWo;  // W_O^T blocks as rows of 128 bytes
+  CUtensorMap tmWoh;
   CUtensorMap tmY;   // Y fp16 [M][N], gated [M][N / 2]: 64 x 128 boxes, 128-byte swizzle (stores)
   CUtensorMap tmZ;   // Z fp16 [M][N], the same boxes
   CUtensorMap tmR;   // residual fp16 [M][N], the same boxes (loads)
@@ -66,9 +74,12 @@ __device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.
 template <int R>
 __device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// Tile t -> (256-channel tile, token tile): token tiles in groups of gm, the
-// token tile fastest (pair_tile_coords).
-__device__ __forceinline__ void fused_tile_coords(const FusedPairArgs& g, int t, int& tn2, int& tm) {
+// Unit u -> (256-channel tile, token tile, half): whole tiles (half -1), then
+// the first and second 128 channels of the tiles that are left.  Token tiles
+// come in groups of gm, the token tile fastest (pair_tile_coords).
+__device__ __forceinline__ void fused_unit_coords(const FusedPairArgs& g, int u, int& tn2, int& tm, int& half) {
+  half = u < g.whole ? -1 : (u - g.whole) & 1;
+  const int t = u < g.whole ? u : g.whole + ((u - g.whole) >> 1);
   const int per = g.gm * g.tiles_n2;
   const int grp = t / per;
   const int w = t - grp * per;
@@ -149,10 +160,15 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
         const uint32_t lfull0 = mapa_shared(smem_u32(&full[0]), 0);
         int gi = 0;
         bool ok = true;
-        for (int t = cid; ok && t < g.tiles; t += g.ncl) {
-          int tn2, tm;
-          fused_tile_coords(g, t, tn2, tm);
-          const int ctile = 2 * tn2 + crk;      // the 128 channels this CTA loads
+        for (int u = cid; ok && u < g.units; u += g.ncl) {
+          int tn2, tm, half;
+          fused_unit_coords(g, u, tn2, tm, half);
+          // the channels this CTA loads: a block of 128, or half of one
+          const int ctile = 2 * tn2 + (half < 0 ? crk : half);
+          const int c0 = half < 0 ? 0 : crk * 64;
+          const CUtensorMap* mapA = half < 0 ? &prm.tmA : &prm.tmAh;
+          const CUtensorMap* mapWo = half < 0 ? &prm.tmWo : &prm.tmWoh;
+          const uint32_t bytes = 2u * (half < 0 ? kPairStage : kPairStage - 8192);
           const int m0 = tm * 256 + crk * 128;  // its 128 tokens
           for (int r = 0; r < T; ++r, ++gi) {
             const int s = gi % S;
@@ -160,18 +176,18 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
               ok = false;
               break;
             }
-            if (leader) mbar_arrive_expect_tx(&full[s], 2u * kPairStage);
+            if (leader) mbar_arrive_expect_tx(&full[s], bytes);
             unsigned char* W = smem + s * kPairStage;
             unsigned char* X = W + 16384;
             const uint32_t lb = lfull0 + static_cast<uint32_t>(8 * s);
             if (r < g.kb) {
-              tma_load_2d_pair(W, &prm.tmA, lb, 0, (ctile * g.kb + r) * 128);
+              tma_load_2d_pair(W, mapA, lb, 0, (ctile * g.kb + r) * 128 + c0);
               tma_load_2d_pair(X, &prm.tmX, lb, r * 128, m0);
             } else {
               const int j = r - g.kb;
               const int lo = j >= g.ncs ? 1 : 0;  // U rows [0, M) hold hi, [M, 2M) hold lo
               const int ib = j - lo * g.ncs;
-              tma_load_2d_pair(W, &prm.tmWo, lb, 0, (ctile * g.ncs + ib) * 128);
+              tma_load_2d_pair(W, mapWo, lb, 0, (ctile * g.ncs + ib) * 128 + c0);
               tma_load_2d_pair(X, &prm.tmU, lb, ib * 64, lo * g.M + m0);
             }
           }
@@ -188,14 +204,14 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
       __syncwarp();
     } else if (warp == 1 && leader) {
       // ---------------------------------------------------------- pair MMA (even CTA)
-      constexpr uint32_t idesc_main = idesc_s8_s32(256, 256);
-      constexpr uint32_t idesc_comp = idesc_f16_f32(256, 256);
       const uint64_t xdesc0 = sdesc_k_sw128(smem_u32(smem + 16384));  // rows: tokens
       const uint64_t wdesc0 = sdesc_k_sw128(smem_u32(smem));          // columns: channels
       int gi = 0, ti = 0;
       bool ok = true, issued = false;
-      for (int t = cid; ok && t < g.tiles; t += g.ncl, ++ti) {
+      for (int u = cid; ok && u < g.units; u += g.ncl, ++ti) {
         const int buf = ti % nbuf, use = ti / nbuf;
+        const uint32_t idesc_main = u < g.whole ? idesc_s8_s32(256, 256) : idesc_s8_s32(256, 128);
+        const uint32_t idesc_comp = u < g.whole ? idesc_f16_f32(256, 256) : idesc_f16_f32(256, 128);
         if (use > 0 && !warp_agree(mbar_wait_cluster_poll(&main_empty[buf], static_cast<uint32_t>(use - 1) & 1u, abort_flag))) {
           ok = false;
           break;
@@ -262,12 +278,23 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
     const int sw = row & 7;
     const int F = EPI == kEpiGated ? g.N >> 1 : g.N;  // channels of Y
     griddep_wait();  // a[] comes from the previous kernel
-    int ti = 0;
+    int ti = 0, tr = 0;  // units of the pair; those with channels of this group
     bool ok = true;
-    for (int t = cid; t < g.tiles; t += g.ncl, ++ti) {
-      int tn2, tm;
-      fused_tile_coords(g, t, tn2, tm);
+    for (int u = cid; u < g.units; u += g.ncl, ++ti) {
+      int tn2, tm, half;
+      fused_unit_coords(g, u, tn2, tm, half);
       const int buf = ti % nbuf, use = ti / nbuf;
+      if (half == 1 - grp) {  // the other group's 128 channels: only give the accumulators back
+        if (ok) ok = mbar_wait(&main_full[buf], static_cast<uint32_t>(use) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&main_empty[buf]), 0));
+        if (comp) {
+          if (ok) ok = mbar_wait(comp_full, static_cast<uint32_t>(ti) & 1u, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(comp_empty), 0));
+        }
+        continue;
+      }
       const int n0 = tn2 * 256 + grp * 128;  // the group's first channel
       const int m0 = tm * 256 + crk * 128;
       const int m = m0 + row;
@@ -308,7 +335,7 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
       if (ok) ok = mbar_wait(&main_full[buf], static_cast<uint32_t>(use) & 1u, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(grp * 128);
+      const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half < 0 ? grp * 128 : 0);
       uint32_t r[128];
       if (ok) {
 #pragma unroll
@@ -379,7 +406,7 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
         if (!residual) take_boxes();
       }
       if (residual) {
-        if (ok) ok = mbar_wait(&res_full[grp], static_cast<uint32_t>(ti) & 1u, abort_flag);
+        if (ok) ok = mbar_wait(&res_full[grp], static_cast<uint32_t>(tr) & 1u, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
       }
       if (EPI == kEpiGated) {
@@ -413,11 +440,12 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
         }
       }
       store_boxes(&prm.tmY, kOut, F);
+      ++tr;
     }
     if (issuer) {
       bulk_wait_group_all();
       // a residual box still on its way (only after a wait gave up) lands before the CTA leaves
-      if (*abort_flag && EPI == kEpiAct && e.residual) drain_ring(&res_full[grp], 1, ti);
+      if (*abort_flag && EPI == kEpiAct && e.residual) drain_ring(&res_full[grp], 1, tr);
     }
   }
   tc_fence_before();

@@ -201,6 +201,17 @@ def test_many_tiles_with_residual(q, oracle, N, nO):
         check_forward(Layer(q, oracle, synth.W8_PERCHANNEL, M, 128, N, nO, gated=True), "gelu", keep_z=True)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("nO", [0, 13])
+@pytest.mark.parametrize("M,N", [(1500, 2064), (2300, 2320), (2900, 1808)])
+def test_whole_and_half_tiles(q, oracle, fmt, nO, M, N):
+    """Fewer tiles than pairs of CTAs, but more than half of them; one wave and
+    a few, a wave and a half: whole tiles alone and before half tiles, with an
+    odd number of 128-channel blocks."""
+    check_forward(Layer(q, oracle, fmt, M, 256, N, nO), "gelu", keep_z=True)
+    check_forward(Layer(q, oracle, fmt, M, 256, N, nO, gated=True), "silu")
+
+
 def test_rows_and_columns_outside_are_left(q, oracle):
     """Nothing behind the last token or the last channel's row is written."""
     for M in (1, 17, 70, 300):
