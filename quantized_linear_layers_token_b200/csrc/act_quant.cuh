@@ -35,20 +35,21 @@ inline int colmax_grid(int M) {
   const int g = (M + kColmaxMinRows - 1) / kColmaxMinRows;
   return g < kColmaxCtas ? g : kColmaxCtas;
 }
-constexpr int kQuantThreads = 512;
+constexpr int kQuantThreads = 512;  // of a row, unless there are many (quant_kernel)
 constexpr int kFusedMomentumMaxM = 64;  // up to this many tokens the update runs inside quant_kernel
 
 
 __device__ __forceinline__ __half2 u32_as_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
-__device__ __forceinline__ float block_max(float v, float* red /* >= kQuantThreads / 32 floats */) {
+template <int T>
+__device__ __forceinline__ float block_max(float v, float* red /* >= T / 32 floats */) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   float r = red[0];
 #pragma unroll
-  for (int w = 1; w < kQuantThreads / 32; ++w) r = fmaxf(r, red[w]);
+  for (int w = 1; w < T / 32; ++w) r = fmaxf(r, red[w]);
   return r;
 }
 
@@ -178,8 +179,8 @@ struct QuantGroup {
   QuantProb pr[MAXP];
 };
 
-// One CTA per token row.  VPT = 8-element vectors per thread
-// (K <= 8 * kQuantThreads * VPT).
+// One CTA of T threads per token row.  VPT = 8-element vectors per thread
+// (K <= 8 * T * VPT).
 // FUSED: every CTA also computes the outlier column maxima over all M rows
 // of its problem and the momentum update itself (identical in every CTA,
 // cheap for small M); the last CTA of the problem to finish writes the new
@@ -190,11 +191,11 @@ struct QuantGroup {
 // the outlier codes x_hat = x / s are computed separately and written over
 // the zeros after a barrier.  O and max|W_O| do not depend on the previous
 // kernel and are read before the grid dependency.
-template <int VPT, bool FUSED, int MAXP>
-__global__ void __launch_bounds__(kQuantThreads)
+template <int T, int VPT, bool FUSED, int MAXP>
+__global__ void __launch_bounds__(T)
 quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
   extern __shared__ __align__(16) unsigned char quant_smem[];
-  __shared__ float red[kQuantThreads / 32];
+  __shared__ float red[T / 32];
   __shared__ int is_last;
   int pi = 0;
   if (MAXP > 1)
@@ -213,11 +214,11 @@ quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
   unsigned* cmx = reinterpret_cast<unsigned*>(xo + nO);             // [nO] fused column maxima (fp32 bits)
 
   griddep_launch_dependents();
-  for (int i = threadIdx.x; i < nO; i += kQuantThreads) {
+  for (int i = threadIdx.x; i < nO; i += T) {
     sO[i] = O[i];
     if (FUSED) cmx[i] = 0u;
   }
-  float wmx = 0.f;  // max|W_O| of outlier threadIdx.x (FUSED, nO <= kQuantThreads handled in the loop below)
+  float wmx = 0.f;  // max|W_O| of outlier threadIdx.x (FUSED, nO <= T handled in the loop below)
   if (FUSED && static_cast<int>(threadIdx.x) < nO) wmx = qp.wmaxO[threadIdx.x];
   griddep_wait();  // X (and s) may come from the previous kernel
   const int m = static_cast<int>(blockIdx.x) - qp.row0;
@@ -225,13 +226,13 @@ quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
   const int nvec = K >> 3;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int vi = threadIdx.x + j * kQuantThreads;
+    const int vi = threadIdx.x + j * T;
     if (vi < nvec) reinterpret_cast<uint4*>(xs)[vi] = __ldg(xv + vi);
   }
-  for (int i = threadIdx.x; i < nO; i += kQuantThreads) sS[i] = s[i];
+  for (int i = threadIdx.x; i < nO; i += T) sS[i] = s[i];
   __syncthreads();
   // set the outliers aside (each thread owns distinct columns)
-  for (int i = threadIdx.x; i < nO; i += kQuantThreads) {
+  for (int i = threadIdx.x; i < nO; i += T) {
     const int col = sO[i];
     xo[i] = h2f(xs[col]);
     xs[col] = 0;
@@ -242,12 +243,12 @@ quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
     // flight, merged with shared-memory atomicMax on the fp32 bit patterns
     // (non-negative, so ordered like unsigned integers)
     const int pairs = M * nO;
-    for (int p0 = threadIdx.x; p0 < pairs; p0 += 8 * kQuantThreads) {
+    for (int p0 = threadIdx.x; p0 < pairs; p0 += 8 * T) {
       uint16_t hv[8];
       int ii[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int p = p0 + u * kQuantThreads;
+        const int p = p0 + u * T;
         ii[u] = -1;
         hv[u] = 0;
         if (p < pairs) {
@@ -262,7 +263,7 @@ quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
         if (ii[u] >= 0) atomicMax(&cmx[ii[u]], __float_as_uint(fabsf(h2f(hv[u]))));
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nO; i += kQuantThreads)
+    for (int i = threadIdx.x; i < nO; i += T)
       sS[i] = momentum_step(sS[i], qg.gamma, __uint_as_float(cmx[i]),
                             i == static_cast<int>(threadIdx.x) ? wmx : qp.wmaxO[i]);
   }
@@ -273,7 +274,7 @@ quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
   __half2 hm = __float2half2_rn(0.f);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int vi = threadIdx.x + j * kQuantThreads;
+    const int vi = threadIdx.x + j * T;
     if (vi < nvec) {
       const uint4 w = reinterpret_cast<const uint4*>(xs)[vi];
       const __half2 m01 = __hmax2(__habs2(u32_as_half2(w.x)), __habs2(u32_as_half2(w.y)));
@@ -282,18 +283,18 @@ quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
     }
   }
   float lmax = fmaxf(__low2float(hm), __high2float(hm));
-  for (int i = threadIdx.x; i < nO; i += kQuantThreads) {
+  for (int i = threadIdx.x; i < nO; i += T) {
     const float f = fabsf(__fdiv_rn(xo[i], sS[i]));
     lmax = f > lmax ? f : lmax;
   }
-  const float amax = block_max(lmax, red);
+  const float amax = block_max<T>(lmax, red);
   const float inv = amax > 0.f ? __fdiv_rn(127.f, amax) : 0.f;
   if (threadIdx.x == 0) qp.a[m] = __fdiv_rn(amax, 127.f);
 
   int8_t* qrow = qp.Xq + static_cast<size_t>(m) * K;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int vi = threadIdx.x + j * kQuantThreads;
+    const int vi = threadIdx.x + j * T;
     if (vi < nvec) {
       const uint4 w = reinterpret_cast<const uint4*>(xs)[vi];
       const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
@@ -309,7 +310,7 @@ quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
   }
   __syncthreads();  // the zero codes at the outlier columns are written before the patch below
   const size_t lo_off = static_cast<size_t>(M) * nOp;  // U holds [2][M][nOp]: hi rows, then lo rows
-  for (int i = threadIdx.x; i < nOp; i += kQuantThreads) {
+  for (int i = threadIdx.x; i < nOp; i += T) {
     if (i < nO) {
       const float xh = __fdiv_rn(xo[i], sS[i]);
       const int q = quant_code(xh, inv);
@@ -327,13 +328,13 @@ quant_kernel(const __grid_constant__ QuantGroup<MAXP> qg) {
   }
   if (FUSED && nO > 0) {
     if (M == 1) {  // the only reader of the old state
-      for (int i = threadIdx.x; i < nO; i += kQuantThreads) s[i] = sS[i];
+      for (int i = threadIdx.x; i < nO; i += T) s[i] = sS[i];
     } else {
       __syncthreads();
       if (threadIdx.x == 0) is_last = (atomicAdd(qp.counter, 1u) == static_cast<unsigned>(M - 1));
       __syncthreads();
       if (is_last) {
-        for (int i = threadIdx.x; i < nO; i += kQuantThreads) s[i] = sS[i];
+        for (int i = threadIdx.x; i < nO; i += T) s[i] = sS[i];
         if (threadIdx.x == 0) *qp.counter = 0u;
       }
     }
