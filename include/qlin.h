@@ -335,6 +335,9 @@ typedef enum {
  *             (for qlin_backward_act), or NULL.
  *   X, s, gamma, update_momentum, workspace  as in qlin_forward; the size is
  *             qlin_forward_act_workspace's.
+ *             What a call leaves zero lies where the layer, the token count and
+ *             the entry point put it: a workspace is zero-filled again before
+ *             it serves another of them (or after it was another call's).
  * Apart from Y and residual no two buffers overlap. */
 QLIN_API qlin_status qlin_forward_act_workspace(int32_t M, const qlin_weights* w, size_t* bytes);
 QLIN_API qlin_status qlin_forward_act(const uint16_t* X, int32_t M, const qlin_weights* w, float* s, float gamma,
