@@ -352,6 +352,10 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused
   GemmPlan p{};
   p.nprob = n;
   p.bt = pick_bt(M);
+  // Fused INT8 layers on CTA pairs from 97 tokens on (4096 -> 4096 at 128
+  // tokens 19.0 against 22.3 us, 1024 -> 1024 10.3 against 12.4; at 70 tokens
+  // of 11008 -> 4096 36 against 30).
+  if (fused && ws[0]->fmt == QLIN_W8_PERCHANNEL && M > 96 && p.bt == 128 && max_bt() == 256) p.bt = 256;
   const int ks = gemm_ks(p.bt);
   bool any_outliers = false;
   unsigned it = 0;
@@ -422,11 +426,16 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused
   off = round_up(off + (p.split ? size_t(p.grid) * 4 : 0), kAlign);
   // A fused launch widens from its second token tile on (10 to 15 % faster at
   // 257 to 511 tokens), except where widening a very large per-channel layer
-  // costs more than it gives (8192 -> 28672 at 300 tokens: 187 against 165 us).
+  // costs more than it gives (8192 -> 28672 at 300 tokens: 187 against 165 us);
+  // and in its first tile of 256 while the layer is small for the tokens (4096
+  // -> 4096 at 129 tokens 25.3 against 28.3 us, at 256 25.4 against 33.5; 1024
+  // -> 1024 14 against 17 and 21; but 4096 -> 11008 at 129 36 against 30).
   int widen_from = widen_min_m();
-  if (fused && widen_from > 257 &&
-      (ws[0]->fmt == QLIN_W4_G128 || static_cast<long long>(ws[0]->K) * ws[0]->N <= 100000000LL))
-    widen_from = 257;
+  if (fused && widen_from > 0) {
+    const long long weights = static_cast<long long>(ws[0]->K) * ws[0]->N;
+    if (widen_from > 257 && (ws[0]->fmt == QLIN_W4_G128 || weights <= 100000000LL)) widen_from = 257;
+    if (widen_from > 129 && weights <= 131072LL * M) widen_from = 129;
+  }
   p.widen = (n == 1 && ws[0]->fmt != QLIN_W8_PERCHANNEL && p.bt == 256 && widen_from > 0 && M >= widen_from) ? 1 : 0;
   p.w8_off = off;
   off = round_up(off + (p.widen ? size_t(p.pr[0].tiles_n) * p.pr[0].kb * 16384 : 0), kAlign);

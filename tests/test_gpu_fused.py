@@ -166,6 +166,22 @@ def test_forward_modes(q, oracle, fmt, knobs):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [96, 97, 129, 200, 256, 257])
+@pytest.mark.parametrize("knobs", [{}, {"widen_min_m": 0}, {"pair_mma": 0}], ids=str)
+def test_first_pair_tile(q, oracle, fmt, M, knobs):
+    """INT4 converted inside the kernel or widened, one CTA or pairs."""
+    with q.knobs(**knobs):
+        check_forward(Layer(q, oracle, fmt, M, 512, 400, 21), "silu", keep_z=True)
+        check_forward(Layer(q, oracle, fmt, M, 512, 400, 0, gated=True), "gelu_tanh")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_first_pair_tile_of_a_large_layer(q, oracle, fmt):
+    """Too many weights to widen at this token count."""
+    check_forward(Layer(q, oracle, fmt, 130, 4096, 4352, 9), "relu")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M", [1, 16, 50, 100, 600])
 def test_plain_epilogue_equals_forward(q, oracle, fmt, M):
     """Without bias, activation and residual: qlin_forward, bit for bit; Z too."""
