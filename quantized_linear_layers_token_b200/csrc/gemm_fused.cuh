@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
     const int F = EPI == kEpiGated ? g.N >> 1 : g.N;  // channels of Y
     griddep_wait();  // a[] comes from the previous kernel
     int ti = 0, tr = 0;  // units of the pair; those with channels of this group
+    int loads = 0;       // the issuer's residual loads, one a unit as long as no wait gives up
     bool ok = true;
     for (int u = cid; u < g.units; u += g.ncl, ++ti) {
       int tn2, tm, half;
@@ -304,8 +305,12 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
         if (issuer) bulk_wait_group_read0();
         named_bar_sync(gbar, 128);
       };
-      // the issuer has taken the boxes: the residual on its way into them
+      // the issuer has taken the boxes: the residual on its way into them.  Not
+      // after a wait gave up: the issuer then no longer waits for a load's
+      // bytes before it would arm the barrier and fill the boxes again.
       auto load_residual = [&] {
+        if (!ok) return;
+        ++loads;
         int n = 0;
         for (int b = 0; b < 2; ++b) n += n0 + 64 * b < g.N && m0 < g.M ? 1 : 0;
         mbar_arrive_expect_tx(&res_full[grp], static_cast<uint32_t>(n) * 16384u);
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(FusedPairCfg::kThreads, 1) gemm_fused_kernel(c
     if (issuer) {
       bulk_wait_group_all();
       // a residual box still on its way (only after a wait gave up) lands before the CTA leaves
-      if (*abort_flag && EPI == kEpiAct && e.residual) drain_ring(&res_full[grp], 1, tr);
+      if (!ok) drain_ring(&res_full[grp], 1, loads);
     }
   }
   tc_fence_before();
