@@ -351,6 +351,9 @@ QLIN_API qlin_status qlin_forward_act(const uint16_t* X, int32_t M, const qlin_w
  *   dbias[n] = sum_m dZ[m][n]
  * and the residual's gradient is dY itself.
  *   Z      the forward's pre-activation; may be NULL when act is QLIN_ACT_NONE.
+ *          An infinity in it (a pre-activation past fp16's range) takes the
+ *          limits: act' 0 and 1, and for the gated block act(-inf) = 0 and
+ *          act(inf) = inf.
  *   dX     device fp16 [M][K], fully overwritten, or NULL; dbias device fp32
  *          [N], fully overwritten, or NULL; at least one of them is wanted.
  *   s      as in qlin_backward_dx.

@@ -15,6 +15,10 @@
 // product undoes it in fp32.  The bias's gradient sums the fp32 dZ.
 #pragma once
 
+#include <math.h>
+
+#include <type_traits>
+
 #include "dx_pair.cuh"
 #include "norm.cuh"
 
@@ -33,8 +37,8 @@ struct DactArgs {
 };
 
 // dZ of 8 channels in fp32 pairs from their packed values: z (8 halves) and
-// dy (8, gated: 4 in x and y).
-template <bool GATED>
+// dy (8, gated: 4 in x and y).  LIMITS as in act_slopes.
+template <bool GATED, bool LIMITS>
 __device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv, f32x2 (&d)[4]) {
   f32x2 z[4];
   h8_to_f2(zv, z);
@@ -45,7 +49,7 @@ __device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv
     const float2 y0 = __half22float2(u32_as_h2(yv.x)), y1 = __half22float2(u32_as_h2(yv.y));
     const f32x2 dy[2] = {f2_pack(y0.x, y0.y), f2_pack(y1.x, y1.y)};
     f32x2 val[2], slope[2];
-    act_slopes<2>(act, gate, val, slope);
+    act_slopes<LIMITS>(act, gate, val, slope);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float2 dg = f2_unpack(f2_mul(f2_mul(dy[i], up[i]), slope[i])), du = f2_unpack(f2_mul(dy[i], val[i]));
@@ -56,7 +60,7 @@ __device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv
     h8_to_f2(yv, d);
     if (act != kActNone) {
       f32x2 val[4], slope[4];
-      act_slopes<4>(act, z, val, slope);
+      act_slopes<LIMITS>(act, z, val, slope);
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[i] = f2_mul(d[i], slope[i]);
     }
@@ -90,9 +94,17 @@ __device__ __forceinline__ void load_fraction(const DactArgs& g, int v, f32x2 (&
   for (int i = 0; i < 4; ++i) m[i] = f2_pack(fraction(c[2 * i]), fraction(c[2 * i + 1]));
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN where either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // A bound on |dZ| of those channels, up to the factor 1.13 of the slopes
-// (and |act(z)| <= |z|).
-template <bool GATED>
+// (and |act(z)| <= |z|).  Gated, an infinity in Z makes it infinite, or NaN
+// beside a zero dY (max_nan keeps that); with LIMITS an infinite gate or up
+// value counts as 65504.
+template <bool GATED, bool LIMITS>
 __device__ __forceinline__ float dact_bound(const uint4 zv, const uint4 yv) {
   if (GATED) {
     const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
@@ -102,7 +114,8 @@ __device__ __forceinline__ float dact_bound(const uint4 zv, const uint4 yv) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __half2 h = __habs2(u32_as_h2(zw[i]));
-      top = fmaxf(top, fabsf(dy[i]) * __half2float(__hmax(__low2half(h), __high2half(h))));
+      const float z = __half2float(__hmax(__low2half(h), __high2half(h)));
+      top = LIMITS ? fmaxf(top, fabsf(dy[i]) * fminf(z, 65504.f)) : max_nan(top, fabsf(dy[i]) * z);
     }
     return top;
   }
@@ -111,8 +124,22 @@ __device__ __forceinline__ float dact_bound(const uint4 zv, const uint4 yv) {
   return fmaxf(__low2float(m), __high2float(m));
 }
 
+// The largest bound of the CTA's threads over nw warps (`red` holds one value
+// a warp and is free again after the next barrier); NaN if one is.
+__device__ __forceinline__ float dact_top(float top, float* red, int nw) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = lane < nw ? red[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return top;
+}
+
 // 2^e with top 2^e in [2^13, 2^14), as its biased exponent: |dZ m_n| 2^e
-// stays below 2^14 * 1.13 * 2.3.  A row of zeros, or one that holds an
+// stays below 2^14 * 1.13 * 2.3.  A row of zeros, or one whose dY holds an
 // infinity, keeps e = 0.
 __device__ __forceinline__ uint32_t dact_exponent(float top) {
   const uint32_t b = __float_as_uint(top) >> 23;
@@ -140,34 +167,36 @@ constexpr int kDactRingThreads = 768;  // at most: 80 registers a thread
 // pass over the row.
 template <bool GATED>
 __global__ void __launch_bounds__(kDactThreads) dact_rows_kernel(const __grid_constant__ DactArgs g) {
-  __shared__ float red[kDactThreads / 32];
+  __shared__ float red[2][32];
   griddep_launch_dependents();
   griddep_wait();
   const size_t m = blockIdx.x;
   const int nv = g.N >> 3;
-  float top = 0.f;
-  for (int v = threadIdx.x; v < nv; v += kDactThreads) {
-    uint4 z, y;
-    dact_load<GATED>(g, m, v, z, y);
-    top = fmaxf(top, dact_bound<GATED>(z, y));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kDactThreads / 32; ++w) top = fmaxf(top, red[w]);
-  const uint32_t e = dact_exponent(top);
-  const float scale = __uint_as_float(e << 23);
-  if (threadIdx.x == 0) g.rowscale[m] = __uint_as_float((254u - e) << 23);
-  for (int v = threadIdx.x; v < nv; v += kDactThreads) {
-    uint4 z, y;
-    f32x2 d[4], c[4];
-    dact_load<GATED>(g, m, v, z, y);
-    dact_vec<GATED>(g.act, z, y, d);
-    load_mant(g, v, c);
-    reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, c);
-  }
+  auto row = [&](auto lim, float* shared) {  // false: infinities that are still to be limited
+    constexpr bool kLimits = decltype(lim)::value;
+    float top = 0.f;
+    for (int v = threadIdx.x; v < nv; v += kDactThreads) {
+      uint4 z, y;
+      dact_load<GATED>(g, m, v, z, y);
+      top = max_nan(top, dact_bound<GATED, kLimits>(z, y));
+    }
+    top = dact_top(top, shared, kDactThreads / 32);
+    if (!kLimits && !(top < INFINITY)) return false;
+    const uint32_t e = dact_exponent(top);
+    const float scale = __uint_as_float(e << 23);
+    if (threadIdx.x == 0) g.rowscale[m] = __uint_as_float((254u - e) << 23);
+    for (int v = threadIdx.x; v < nv; v += kDactThreads) {
+      uint4 z, y;
+      f32x2 d[4], c[4];
+      dact_load<GATED>(g, m, v, z, y);
+      dact_vec<GATED, kLimits>(g.act, z, y, d);
+      load_mant(g, v, c);
+      reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, c);
+    }
+    return true;
+  };
+  // (not gated: the bound does not see Z)
+  if (!GATED || !row(std::false_type{}, red[0])) row(std::true_type{}, red[1]);
 }
 
 // Partial column sums of dZ: thread t of CTA (x, y) owns the 8 channels of
@@ -184,7 +213,7 @@ __global__ void __launch_bounds__(128) dact_columns_kernel(const __grid_constant
     uint4 z, y;
     f32x2 d[4];
     dact_load<GATED>(g, m, v, z, y);
-    dact_vec<GATED>(g.act, z, y, d);
+    dact_vec<GATED, true>(g.act, z, y, d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = f2_add(s[i], d[i]);
   }
@@ -205,7 +234,7 @@ template <bool GATED, int VPT, bool ACC>
 __global__ void __launch_bounds__(kDactRingThreads) dact_ring_kernel(const __grid_constant__ DactArgs g) {
   constexpr bool kKeep = VPT * (ACC ? 2 : 1) <= 4;
   extern __shared__ __align__(128) unsigned char ring_smem[];
-  __shared__ float red[2][32];
+  __shared__ float red[3][32];
   __shared__ uint64_t full[kRingStages];
   __shared__ int abort_flag;
   const int t = threadIdx.x, T = static_cast<int>(blockDim.x), nw = T >> 5;
@@ -272,51 +301,53 @@ __global__ void __launch_bounds__(kDactRingThreads) dact_ring_kernel(const __gri
         y = reinterpret_cast<const uint4*>(yr)[v];
       }
     };
-    float top = 0.f;
+    auto bound = [&](auto lim, float* shared) {
+      float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (t + j * T < nv) {
-        uint4 z, y;
-        values(t + j * T, z, y);
-        top = fmaxf(top, dact_bound<GATED>(z, y));
+      for (int j = 0; j < VPT; ++j) {
+        if (t + j * T < nv) {
+          uint4 z, y;
+          values(t + j * T, z, y);
+          top = max_nan(top, dact_bound<GATED, decltype(lim)::value>(z, y));
+        }
       }
-    }
+      return dact_top(top, shared, nw);
+    };
+    auto write = [&](auto lim, float top) {
+      const uint32_t ex = dact_exponent(top);
+      const float scale = __uint_as_float(ex << 23);
+      if (t == 0 && g.dZ) g.rowscale[m] = __uint_as_float((254u - ex) << 23);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((t & 31) == 0) red[i & 1][t >> 5] = top;
-    __syncthreads();
-    top = (t & 31) < nw ? red[i & 1][t & 31] : 0.f;
+      for (int j = 0; j < VPT; ++j) {
+        const int v = t + j * T;
+        if (v < nv) {
+          uint4 z, y;
+          f32x2 d[4];
+          values(v, z, y);
+          dact_vec<GATED, decltype(lim)::value>(g.act, z, y, d);
+          if (ACC) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int e = 0; e < 4; ++e) sum[j][e] = f2_add(sum[j][e], d[e]);
+          }
+          if (g.dZ) {
+            f32x2 c[4];
+            if (!kKeep) {
+              if (inside) load_fraction(g, v, c);
+              else load_mant(g, v, c);
+            }
+            reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, kKeep ? mant[kKeep ? j : 0] : c);
+          }
+        }
+      }
+    };
+    const float top = bound(std::bool_constant<!GATED>{}, red[i & 1]);
     if (t == 0 && i > 0 && abort_flag == 0) {  // the previous row's stage: every thread is done with it
       const size_t next = m + static_cast<size_t>(S - 1) * step;
       if (next < M) load(next, (i - 1) % S);
     }
-    const uint32_t ex = dact_exponent(top);
-    const float scale = __uint_as_float(ex << 23);
-    if (t == 0 && g.dZ) g.rowscale[m] = __uint_as_float((254u - ex) << 23);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = t + j * T;
-      if (v < nv) {
-        uint4 z, y;
-        f32x2 d[4];
-        values(v, z, y);
-        dact_vec<GATED>(g.act, z, y, d);
-        if (ACC) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[j][e] = f2_add(sum[j][e], d[e]);
-        }
-        if (g.dZ) {
-          f32x2 c[4];
-          if (!kKeep) {
-            if (inside) load_fraction(g, v, c);
-            else load_mant(g, v, c);
-          }
-          reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, kKeep ? mant[kKeep ? j : 0] : c);
-        }
-      }
-    }
+    // gated: infinities in the row, or NaN, take the bound again (not gated it does not see Z)
+    if (GATED && top < INFINITY) write(std::false_type{}, top);
+    else write(std::true_type{}, GATED ? bound(std::true_type{}, red[2]) : top);
   }
   if (t == 0 && abort_flag) drain_ring(full, S, issued);  // no copy outlives the CTA
   if (ACC) {

@@ -87,9 +87,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluTanhA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluTanhB = 0.044715f;
 
-// z + 0.044715 z^3 and z^2
-__device__ __forceinline__ f32x2 gelu_cubic(f32x2 z, f32x2& z2) {
-  z2 = f2_mul(z, z);
+// z + 0.044715 z^3 from z and z^2
+__device__ __forceinline__ f32x2 gelu_cubic(f32x2 z, f32x2 z2) {
   return f2_fma(f2_mul(z, f2_both(kGeluTanhB)), z2, z);
 }
 
@@ -130,10 +129,8 @@ __device__ __forceinline__ void act_pairs(int act, f32x2 (&z)[N]) {
       break;
     case kActGeluTanh:
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        f32x2 z2;
-        z[i] = f2_mul(z[i], logistic2(f2_mul(gelu_cubic(z[i], z2), f2_both(-kGeluTanhA * kLog2e))));
-      }
+      for (int i = 0; i < N; ++i)
+        z[i] = f2_mul(z[i], logistic2(f2_mul(gelu_cubic(z[i], f2_mul(z[i], z[i])), f2_both(-kGeluTanhA * kLog2e))));
       break;
     case kActSilu:
 #pragma unroll
@@ -158,10 +155,26 @@ __device__ __forceinline__ void act_values(int act, float (&z)[N]) {
   }
 }
 
-// act(z) and act'(z) of N pairs.
-template <int N>
+// act(z) and act'(z) of N pairs, z kept in fp16.  A pre-activation past fp16's
+// range arrives as an infinity and takes the limits -- slopes 0 and 1,
+// act(-inf) = 0, act(inf) = inf -- so no product of an infinity and a vanishing
+// factor may be formed: with LIMITS, z is held within +-65504 beside the
+// factors that vanish (a NaN stays one through them).  Without, z is finite or
+// NaN.
+template <bool LIMITS, int N>
 __device__ __forceinline__ void act_slopes(int act, const f32x2 (&z)[N], f32x2 (&value)[N], f32x2 (&slope)[N]) {
   const f32x2 one = f2_both(1.f);
+  f32x2 above[N], inside[N];  // z from -65504 up; within +-65504
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    above[i] = inside[i] = z[i];
+    if (LIMITS) {
+      const float2 v = f2_unpack(z[i]);
+      const float2 a = make_float2(fmaxf(v.x, -65504.f), fmaxf(v.y, -65504.f));
+      above[i] = f2_pack(a.x, a.y);
+      inside[i] = f2_pack(fminf(a.x, 65504.f), fminf(a.y, 65504.f));
+    }
+  }
   switch (act) {
     case kActRelu:
 #pragma unroll
@@ -176,17 +189,17 @@ __device__ __forceinline__ void act_slopes(int act, const f32x2 (&z)[N], f32x2 (
       for (int i = 0; i < N; ++i) {
         f32x2 e;
         const f32x2 p = normal_cdf(z[i], e);
-        value[i] = f2_mul(z[i], p);
-        slope[i] = f2_fma(f2_mul(z[i], f2_both(0.3989422804014327f)), e, p);
+        value[i] = f2_mul(above[i], p);
+        slope[i] = f2_fma(f2_mul(inside[i], f2_both(0.3989422804014327f)), e, p);
       }
       break;
     case kActGeluTanh:
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        f32x2 z2;
+        const f32x2 z2 = f2_mul(inside[i], inside[i]);
         const f32x2 p = logistic2(f2_mul(gelu_cubic(z[i], z2), f2_both(-kGeluTanhA * kLog2e)));
-        value[i] = f2_mul(z[i], p);
-        const f32x2 q = f2_mul(value[i], f2_fma(p, f2_both(-1.f), one));  // z p (1 - p)
+        value[i] = f2_mul(above[i], p);
+        const f32x2 q = f2_mul(f2_mul(inside[i], p), f2_fma(p, f2_both(-1.f), one));  // z p (1 - p)
         slope[i] = f2_fma(q, f2_fma(z2, f2_both(3.f * kGeluTanhA * kGeluTanhB), f2_both(kGeluTanhA)), p);
       }
       break;
@@ -194,8 +207,8 @@ __device__ __forceinline__ void act_slopes(int act, const f32x2 (&z)[N], f32x2 (
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const f32x2 p = logistic2(f2_mul(z[i], f2_both(-kLog2e)));
-        value[i] = f2_mul(z[i], p);
-        slope[i] = f2_fma(value[i], f2_fma(p, f2_both(-1.f), one), p);  // p + z p (1 - p)
+        value[i] = f2_mul(above[i], p);
+        slope[i] = f2_fma(f2_mul(inside[i], p), f2_fma(p, f2_both(-1.f), one), p);  // p + z p (1 - p)
       }
       break;
     default:
