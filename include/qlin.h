@@ -38,10 +38,13 @@
  *     g128 format K % 128 == 0; 0 <= n_outlier <= min(K, 4096).
  *   - Workspaces: buffers whose size comes from the matching *_workspace
  *     call.  A workspace must be zero-filled before its first use (for
- *     example with cudaMemsetAsync); every successful call leaves it
- *     zero-filled again in the parts that must start at zero, so it can be
- *     reused by later calls on the same stream without clearing.  Calls that
- *     share a workspace must not overlap on the GPU.
+ *     example with cudaMemsetAsync; the first QLIN_WORKSPACE_HEAD bytes
+ *     suffice); every successful call leaves these bytes zero again, so it can
+ *     be reused by later calls on the same stream without clearing, whatever
+ *     their layer, token count and entry point.  Exceptions are the calls whose
+ *     description says that no zero-fill is needed and that the buffer's first
+ *     bytes are overwritten (GPTQ, smoothing search, OffQ).  Calls that share a
+ *     workspace must not overlap on the GPU.
  *   - No entry point is thread-hostile; concurrent calls on different
  *     streams must use different outputs and workspaces.
  */
@@ -60,6 +63,8 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+#define QLIN_WORKSPACE_HEAD 18688 /* bytes that must be zero at the start of a workspace */
 
 typedef enum {
   QLIN_OK = 0,
@@ -335,9 +340,6 @@ typedef enum {
  *             (for qlin_backward_act), or NULL.
  *   X, s, gamma, update_momentum, workspace  as in qlin_forward; the size is
  *             qlin_forward_act_workspace's.
- *             What a call leaves zero lies where the layer, the token count and
- *             the entry point put it: a workspace is zero-filled again before
- *             it serves another of them (or after it was another call's).
  * Apart from Y and residual no two buffers overlap. */
 QLIN_API qlin_status qlin_forward_act_workspace(int32_t M, const qlin_weights* w, size_t* bytes);
 QLIN_API qlin_status qlin_forward_act(const uint16_t* X, int32_t M, const qlin_weights* w, float* s, float gamma,
@@ -358,7 +360,8 @@ QLIN_API qlin_status qlin_forward_act(const uint16_t* X, int32_t M, const qlin_w
  *          [N], fully overwritten, or NULL; at least one of them is wanted.
  *   s      as in qlin_backward_dx.
  *   workspace  qlin_backward_act_workspace bytes, 256-byte aligned; no
- *          zero-fill needed.
+ *          zero-fill needed, and its first QLIN_WORKSPACE_HEAD bytes are left
+ *          as they are.
  * Arithmetic: dZ is formed in fp32 and rounded to fp16 once, multiplied by
  * the mantissa of c'_n and by a power of two of its row that keeps it in
  * range whatever the gradients' scale; the outlier rows of Weff are rounded
@@ -430,7 +433,8 @@ QLIN_API qlin_status qlin_norm_forward(const uint16_t* X, int32_t M, int32_t K, 
  *   dX     device fp16 [M][K] or NULL; may be the buffer of dY, X or dres.
  *   dgamma, dbeta  device fp32 [K] or NULL; at least one output is wanted.
  *   workspace  qlin_norm_backward_workspace bytes, 256-byte aligned, needed
- *          when dgamma or dbeta is wanted; no zero-fill needed.
+ *          when dgamma or dbeta is wanted; no zero-fill needed, and its first
+ *          QLIN_WORKSPACE_HEAD bytes are left as they are.
  * M = 0 writes zeros to dgamma and dbeta. */
 QLIN_API qlin_status qlin_norm_backward_workspace(int32_t M, int32_t K, size_t* bytes);
 QLIN_API qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M, int32_t K, int32_t kind,
@@ -463,7 +467,8 @@ QLIN_API qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, i
  *   singular device int32 (may be NULL): 1 if a pivot of H was zero (H is
  *            singular; W, codes and Hinv are then undefined), else 0.
  *   workspace  qlin_gptq_workspace bytes (one K x K fp64 matrix and a
- *            little scratch), 256-byte aligned; no zero-fill needed.
+ *            little scratch), 256-byte aligned; no zero-fill needed, and its
+ *            first bytes are overwritten.
  * K <= 16384.  The call enqueues 4 K + 3 small kernels on `stream`. */
 QLIN_API qlin_status qlin_gptq_workspace(int32_t K, int32_t N, size_t* bytes);
 QLIN_API qlin_status qlin_gptq_quantize(const double* X, int32_t ns, int32_t K, int32_t N, double* W,
@@ -489,7 +494,7 @@ QLIN_API qlin_status qlin_gptq_quantize(const double* X, int32_t ns, int32_t K, 
  *   best    device int32 (may be NULL): the first j of least loss.
  *   s_best  device fp32 [K] (may be NULL): s of that candidate, 1 off T.
  *   workspace  qlin_smooth_search_workspace bytes, 256-byte aligned (no
- *           zero-fill needed).
+ *           zero-fill needed; its first bytes are overwritten).
  * Shapes: as the W4A8 per-channel layer (K % 32 == 0, N % 16 == 0), M >= 1,
  * 1 <= G <= 64. */
 QLIN_API qlin_status qlin_smooth_search_workspace(int32_t M, int32_t K, int32_t N, int32_t G, size_t* bytes);
@@ -550,15 +555,16 @@ QLIN_API qlin_status qlin_offq_quant_act(const uint16_t* X, int32_t M, int32_t K
 
 /* The GEMM from quantized activations: Y device fp16 [M][N] as above.  The
  * workspace (qlin_offq_gemm_workspace bytes, 256-byte aligned, no
- * zero-fill needed) receives the codes widened to INT8 (16 q_w) once per
- * call. */
+ * zero-fill needed, its first bytes are overwritten) receives the codes
+ * widened to INT8 (16 q_w) once per call. */
 QLIN_API qlin_status qlin_offq_gemm_workspace(int32_t M, int32_t K, int32_t N, size_t* bytes);
 QLIN_API qlin_status qlin_offq_gemm(const int8_t* Xq, const float* scale, const float* offset, int32_t M, int32_t K,
                                     int32_t N, const uint8_t* codes, const float* chan_scale, const float* colsum,
                                     uint16_t* Y, void* workspace, size_t ws_bytes, void* stream);
 
 /* qlin_offq_quant_act then qlin_offq_gemm, the intermediates in the
- * workspace (qlin_offq_forward_workspace bytes, 256-byte aligned). */
+ * workspace (qlin_offq_forward_workspace bytes, 256-byte aligned; no
+ * zero-fill needed, its first bytes are overwritten). */
 QLIN_API qlin_status qlin_offq_forward_workspace(int32_t M, int32_t K, int32_t N, size_t* bytes);
 QLIN_API qlin_status qlin_offq_forward(const uint16_t* X, int32_t M, int32_t K, int32_t N, const int8_t* signs,
                                        const uint8_t* codes, const float* chan_scale, const float* colsum,

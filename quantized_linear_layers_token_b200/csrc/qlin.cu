@@ -55,6 +55,20 @@ qlin_status fail(qlin_status st, const char* fmt, ...) {
   } while (0)
 
 constexpr size_t kAlign = 256;
+
+// What every workspace starts with, wherever its call puts the rest: all that
+// must be zero on entry and is left zero, at one place for every layer, token
+// count and entry point, so that any of them may follow another on a workspace.
+struct WorkspaceHead {
+  unsigned cnt[512];       // counters of split tiles: one per persistent CTA of the GEMM, two per split
+                           // tile of a launch on CTA pairs, one per split tile of the input gradient
+  unsigned momentum[64];   // completion counter of each problem's momentum update
+  unsigned cmax[4096];     // outlier column maxima, as many as a layer may have
+};
+constexpr int kHeadCounters = 512;
+static_assert(sizeof(WorkspaceHead) == QLIN_WORKSPACE_HEAD && QLIN_WORKSPACE_HEAD % kAlign == 0, "include/qlin.h");
+static_assert(kMaxGrid <= kHeadCounters && 2 * 2 * kMaxPairs <= kHeadCounters && kMaxProbs <= 64, "counters of a launch");
+WorkspaceHead* head_of(void* workspace) { return static_cast<WorkspaceHead*>(workspace); }
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int pad8(int n) { return (n + 7) / 8 * 8; }
@@ -252,13 +266,13 @@ struct GemmPlan {
   int bt, grid, split, widen, nprob;
   long long tiles;         // tiles of every problem
   GemmProb pr[kMaxProbs];  // per problem: shape, tiles and iteration offsets (pointers unset)
-  size_t acc_off, comp_off, cnt_off, w8_off, total;  // shared scratch (after the problems' U operands)
+  size_t acc_off, comp_off, w8_off, total;  // shared scratch (after the problems' U operands)
   size_t u_off[kMaxProbs];                           // each problem's compensation operand U
   // CTA-pair launch (one problem, 256 x 256 tiles): pairs, whole tiles and
-  // the stream-K tail's step boundaries, partial slots and tile counters
+  // the stream-K tail's step boundaries and partial slots
   int pair_ncl, pair_dp;
   long long pair_sk_tiles;
-  size_t pacc_off, pcomp_off, pcnt_off;
+  size_t pacc_off, pcomp_off;
   unsigned pair_bnd[kMaxPairs + 1];
 };
 
@@ -422,8 +436,6 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused
   off = round_up(off + (p.split ? size_t(2) * p.grid * slot_bytes : 0), kAlign);
   p.comp_off = off;
   off = round_up(off + (p.split && any_outliers ? size_t(2) * p.grid * slot_bytes : 0), kAlign);
-  p.cnt_off = off;
-  off = round_up(off + (p.split ? size_t(p.grid) * 4 : 0), kAlign);
   // A fused launch widens from its second token tile on (10 to 15 % faster at
   // 257 to 511 tokens), except where widening a very large per-channel layer
   // costs more than it gives (8192 -> 28672 at 300 tokens: 187 against 165 us);
@@ -442,7 +454,7 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused
   p.pair_ncl = 0;
   p.pair_dp = 0;
   p.pair_sk_tiles = 0;
-  p.pacc_off = p.pcomp_off = p.pcnt_off = off;
+  p.pacc_off = p.pcomp_off = off;
   if (n == 1 && use_pair(p, ws[0])) {
     const GemmProb& q = p.pr[0];
     const bool conv = p.widen && M <= convert_max_m() && !fused;
@@ -466,13 +478,18 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused
       off = round_up(off + size_t(2) * p.pair_ncl * part, kAlign);
       p.pcomp_off = off;
       off = round_up(off + (ws[0]->n_outlier > 0 ? size_t(p.pair_ncl) * part : 0), kAlign);
-      p.pcnt_off = off;
-      off = round_up(off + size_t(p.pair_sk_tiles) * 2 * 4, kAlign);
     }
   }
   p.total = off;
   return p;
 }
+
+// A GEMM launch's scratch (laid out by the plan) and the counters of its split
+// tiles, zero on entry and left zero.
+struct GemmScratch {
+  char* p;
+  unsigned* cnt;
+};
 
 GemmPlan plan_gemm(int M, const qlin_weights* w, bool fused = false) { return plan_gemm_group(M, &w, 1, fused); }
 
@@ -632,7 +649,7 @@ bool use_pair(const GemmPlan& p, const qlin_weights* w) {
 // converted inside the kernel.
 template <int FMT>
 qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
-                             int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream) {
+                             int32_t* acc_debug, const GemmScratch& gws, const uint8_t* codes8, float cmul, cudaStream_t stream) {
   PairParams prm;
   memset(&prm, 0, sizeof(prm));
   PairArgs& g = prm.g;
@@ -665,9 +682,9 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
   g.ncl = p.pair_ncl;
   g.dp = p.pair_dp;
   for (int c = 0; c <= kMaxPairs; ++c) g.bnd[c] = p.pair_bnd[c];
-  g.ws_acc = reinterpret_cast<int32_t*>(gws + p.pacc_off);
-  g.ws_comp = reinterpret_cast<float*>(gws + p.pcomp_off);
-  g.ws_cnt = reinterpret_cast<unsigned*>(gws + p.pcnt_off);
+  g.ws_acc = reinterpret_cast<int32_t*>(gws.p + p.pacc_off);
+  g.ws_comp = reinterpret_cast<float*>(gws.p + p.pcomp_off);
+  g.ws_cnt = gws.cnt;
   qlin_status st = QLIN_OK;
   if (FMT == kFmtW8) {
     st = make_map(&prm.tmA, codes8, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128,
@@ -677,7 +694,7 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
   st = make_map(&prm.tmX, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->K, M, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != QLIN_OK) return st;
   if (w->n_outlier > 0) {
-    st = make_map(&prm.tmU, gws + p.u_off[0], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->n_outlier_pad,
+    st = make_map(&prm.tmU, gws.p + p.u_off[0], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->n_outlier_pad,
                   2 * static_cast<uint64_t>(M), 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != QLIN_OK) return st;
     st = make_map(&prm.tmWo, w->W_Ot, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128,
@@ -698,7 +715,7 @@ qlin_status launch_gemm_pair(const GemmPlan& p, const qlin_weights* w, const int
 // format, or INT4 widened ahead).
 template <int EPI, int ACT>
 qlin_status launch_fused_t(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
-                           char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream, const EpiArgs& epi) {
+                           const GemmScratch& gws, const uint8_t* codes8, float cmul, cudaStream_t stream, const EpiArgs& epi) {
   FusedPairParams prm;
   memset(&prm, 0, sizeof(prm));
   FusedPairArgs& g = prm.g;
@@ -730,7 +747,7 @@ qlin_status launch_fused_t(const GemmPlan& p, const qlin_weights* w, const int8_
   st = make_map(&prm.tmX, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->K, M, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != QLIN_OK) return st;
   if (w->n_outlier > 0) {
-    st = make_map(&prm.tmU, gws + p.u_off[0], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->n_outlier_pad,
+    st = make_map(&prm.tmU, gws.p + p.u_off[0], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->n_outlier_pad,
                   2 * static_cast<uint64_t>(M), 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != QLIN_OK) return st;
     for (int h = 0; h < 2 && st == QLIN_OK; ++h)
@@ -761,7 +778,7 @@ qlin_status launch_fused_t(const GemmPlan& p, const qlin_weights* w, const int8_
 
 template <int EPI>
 qlin_status launch_fused_act(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
-                             char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream, const EpiArgs& epi) {
+                             const GemmScratch& gws, const uint8_t* codes8, float cmul, cudaStream_t stream, const EpiArgs& epi) {
   switch (epi.act) {
     case kActRelu: return launch_fused_t<EPI, kActRelu>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
     case kActGelu: return launch_fused_t<EPI, kActGelu>(p, w, Xq, a, Y, gws, codes8, cmul, stream, epi);
@@ -773,7 +790,7 @@ qlin_status launch_fused_act(const GemmPlan& p, const qlin_weights* w, const int
 
 // INT8 operands on CTA pairs, with the epilogue variant chosen at run time.
 qlin_status launch_pair_w8(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
-                           int32_t* acc_debug, char* gws, const uint8_t* codes8, float cmul, cudaStream_t stream,
+                           int32_t* acc_debug, const GemmScratch& gws, const uint8_t* codes8, float cmul, cudaStream_t stream,
                            const EpiArgs* epi, int variant) {
   if (variant == kEpiGated) return launch_fused_act<kEpiGated>(p, w, Xq, a, Y, gws, codes8, cmul, stream, *epi);
   if (variant == kEpiAct) return launch_fused_act<kEpiAct>(p, w, Xq, a, Y, gws, codes8, cmul, stream, *epi);
@@ -787,7 +804,7 @@ qlin_status launch_pair_w8(const GemmPlan& p, const qlin_weights* w, const int8_
 // `variant`: a fused epilogue (one problem, no acc_debug).
 template <int MAXP>
 qlin_status launch_gemm_group(const GemmPlan& p, const qlin_weights* const* ws, const int8_t* const* Xq,
-                              const float* const* a, uint16_t* const* Y, int32_t* const* acc_debug, char* gws,
+                              const float* const* a, uint16_t* const* Y, int32_t* const* acc_debug, const GemmScratch& gws,
                               cudaStream_t stream, const EpiArgs* epi = nullptr, int variant = kEpiPlain) {
   qlin_status st = get_encoder();
   if (st != QLIN_OK) return st;
@@ -814,15 +831,15 @@ qlin_status launch_gemm_group(const GemmPlan& p, const qlin_weights* const* ws, 
                   CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != QLIN_OK) return st;
     if (w->n_outlier > 0) {
-      st = make_map(&prm.tmU[q], gws + p.u_off[q], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->n_outlier_pad,
+      st = make_map(&prm.tmU[q], gws.p + p.u_off[q], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->n_outlier_pad,
                     2 * static_cast<uint64_t>(M), 64, p.bt, CU_TENSOR_MAP_SWIZZLE_128B);
       if (st != QLIN_OK) return st;
     }
   }
   if (iters >= (1LL << 31)) return fail(QLIN_ERR_SHAPE, "problem too large (%lld tile iterations)", iters);
-  args.ws_acc = reinterpret_cast<int32_t*>(gws + p.acc_off);
-  args.ws_comp = reinterpret_cast<float*>(gws + p.comp_off);
-  args.ws_cnt = reinterpret_cast<unsigned*>(gws + p.cnt_off);
+  args.ws_acc = reinterpret_cast<int32_t*>(gws.p + p.acc_off);
+  args.ws_comp = reinterpret_cast<float*>(gws.p + p.comp_off);
+  args.ws_cnt = gws.cnt;
   args.nprob = p.nprob;
   args.grid = p.grid;
   args.split = p.split;
@@ -845,7 +862,7 @@ qlin_status launch_gemm_group(const GemmPlan& p, const qlin_weights* const* ws, 
   }
   if (p.widen) {
     const qlin_weights* w = ws[0];
-    uint8_t* w8 = reinterpret_cast<uint8_t*>(gws + p.w8_off);
+    uint8_t* w8 = reinterpret_cast<uint8_t*>(gws.p + p.w8_off);
     const unsigned nblk = static_cast<unsigned>(p.pr[0].tiles_n) * static_cast<unsigned>(p.pr[0].kb);
     const uint8_t* codes = static_cast<const uint8_t*>(w->codes);
     const uint16_t* rf = reinterpret_cast<const uint16_t*>(w->fold_ratio);
@@ -884,14 +901,14 @@ qlin_status launch_gemm_group(const GemmPlan& p, const qlin_weights* const* ws, 
 
 // Single-problem GEMM launch.
 qlin_status launch_gemm(const qlin_weights* w, const int8_t* Xq, const float* a, int M, uint16_t* Y,
-                        int32_t* acc_debug, char* gws, cudaStream_t stream) {
+                        int32_t* acc_debug, const GemmScratch& gws, cudaStream_t stream) {
   const GemmPlan p = plan_gemm(M, w);
   return launch_gemm_group<1>(p, &w, &Xq, &a, &Y, acc_debug ? &acc_debug : nullptr, gws, stream);
 }
 
 // Single-problem GEMM launch with a fused epilogue.
 qlin_status launch_gemm_fused(const GemmPlan& p, const qlin_weights* w, const int8_t* Xq, const float* a, uint16_t* Y,
-                              char* gws, cudaStream_t stream, const EpiArgs& epi, int variant) {
+                              const GemmScratch& gws, cudaStream_t stream, const EpiArgs& epi, int variant) {
   return launch_gemm_group<1>(p, &w, &Xq, &a, &Y, nullptr, gws, stream, &epi, variant);
 }
 
@@ -903,9 +920,7 @@ int fused_momentum_max_m() { return static_cast<int>(knob(QLIN_KNOB_FUSED_MOMENT
 
 constexpr int kQuantSmemMax = 232448 - 1024;  // 227 KB per CTA, less room for the kernel's static shared memory
 
-size_t act_ws_bytes(const qlin_weights* w) {
-  return w->n_outlier > 0 ? round_up(size_t(w->n_outlier) * 4 + 4, kAlign) : 0;
-}
+size_t act_ws_bytes(const qlin_weights* w) { return w->n_outlier > 0 ? sizeof(WorkspaceHead) : 0; }
 
 // Activations of one quantization problem (outputs and scratch per problem).
 struct QuantIO {
@@ -915,7 +930,8 @@ struct QuantIO {
   float* a;
   int8_t* XqO;
   uint16_t* U;   // compensation operand (qlin_forward), or null
-  void* act_ws;  // outlier column maxima + completion counter (update only)
+  unsigned* cmax;     // outlier column maxima and completion counter (update only):
+  unsigned* counter;  // zero on entry, left zero
 };
 
 template <int T, int VPT, bool FUSED, int MAXP>
@@ -968,7 +984,6 @@ qlin_status launch_quant_group(const qlin_weights* const* ws, const QuantIO* io,
     const qlin_weights* w = ws[q];
     const int K = w->K, nO = w->n_outlier;
     QuantProb& p = qg.pr[q];
-    unsigned* cmax = static_cast<unsigned*>(io[q].act_ws);
     p.X = io[q].X;
     p.O = static_cast<const int32_t*>(w->outlier_idx);
     p.s = io[q].s;
@@ -977,7 +992,7 @@ qlin_status launch_quant_group(const qlin_weights* const* ws, const QuantIO* io,
     p.XqO = io[q].XqO;
     p.U = io[q].U;
     p.wmaxO = w->wmax_O;
-    p.counter = cmax ? cmax + nO : nullptr;
+    p.counter = io[q].counter;
     p.K = K;
     p.nO = nO;
     p.nOp = w->n_outlier_pad;
@@ -999,11 +1014,10 @@ qlin_status launch_quant_group(const qlin_weights* const* ws, const QuantIO* io,
       const qlin_weights* w = ws[q];
       const int nO = w->n_outlier;
       if (nO == 0) continue;
-      unsigned* cmax = static_cast<unsigned*>(io[q].act_ws);
       const int grid = colmax_grid(M);
       cudaError_t e = launch_k(colmax_kernel, dim3(grid), dim3(256), size_t(nO) * 8, stream, io[q].X, M, w->K,
-                               static_cast<const int32_t*>(w->outlier_idx), nO, cmax, 1,
-                               static_cast<const float*>(w->wmax_O), io[q].s, gamma, cmax + nO);
+                               static_cast<const int32_t*>(w->outlier_idx), nO, io[q].cmax, 1,
+                               static_cast<const float*>(w->wmax_O), io[q].s, gamma, io[q].counter);
       if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "colmax_kernel launch failed: %s", cudaGetErrorString(e));
     }
   }
@@ -1013,8 +1027,8 @@ qlin_status launch_quant_group(const qlin_weights* const* ws, const QuantIO* io,
 }
 
 qlin_status launch_quant(const uint16_t* X, int M, const qlin_weights* w, float* s, float gamma, int update,
-                         int8_t* Xq, float* a, int8_t* XqO, uint16_t* U, void* act_ws, cudaStream_t stream) {
-  const QuantIO io{X, s, Xq, a, XqO, U, act_ws};
+                         int8_t* Xq, float* a, int8_t* XqO, uint16_t* U, unsigned* cmax, unsigned* counter, cudaStream_t stream) {
+  const QuantIO io{X, s, Xq, a, XqO, U, cmax, counter};
   return launch_quant_group<1>(&w, &io, 1, M, gamma, update, stream);
 }
 
@@ -1023,13 +1037,12 @@ size_t gemm_ws_bytes(int M, const qlin_weights* w, bool fused = false) {
 }
 
 struct FwdLayout {
-  size_t act, xq, a, xqo, gemm, total;
+  size_t xq, a, xqo, gemm, total;
 };
 
 FwdLayout forward_layout(int M, const qlin_weights* w, bool fused = false) {
   FwdLayout L{};
-  size_t off = 0;
-  L.act = off; off = round_up(off + act_ws_bytes(w), kAlign);
+  size_t off = sizeof(WorkspaceHead);
   L.xq = off; off = round_up(off + size_t(M) * w->K, kAlign);
   L.a = off; off = round_up(off + size_t(M) * 4, kAlign);
   L.xqo = off; off = round_up(off + size_t(M) * w->n_outlier, kAlign);
@@ -1038,21 +1051,19 @@ FwdLayout forward_layout(int M, const qlin_weights* w, bool fused = false) {
   return L;
 }
 
-// Workspace of a grouped forward: per problem the quantization scratch, Xq,
-// a and XqO, then the GEMM launch's scratch (every problem's U and the
+// Workspace of a grouped forward: the head, per problem Xq, a and XqO, then the GEMM launch's scratch (every problem's U and the
 // shared split-K slots and counters).
 struct GroupLayout {
-  size_t act[kMaxProbs], xq[kMaxProbs], a[kMaxProbs], xqo[kMaxProbs];
+  size_t xq[kMaxProbs], a[kMaxProbs], xqo[kMaxProbs];
   size_t gemm, total;
   GemmPlan plan;
 };
 
 GroupLayout group_layout(int M, const qlin_weights* const* ws, int n) {
   GroupLayout L{};
-  size_t off = 0;
+  size_t off = sizeof(WorkspaceHead);
   for (int q = 0; q < n; ++q) {
     const qlin_weights* w = ws[q];
-    L.act[q] = off; off = round_up(off + act_ws_bytes(w), kAlign);
     L.xq[q] = off; off = round_up(off + size_t(M) * w->K, kAlign);
     L.a[q] = off; off = round_up(off + size_t(M) * 4, kAlign);
     L.xqo[q] = off; off = round_up(off + size_t(M) * w->n_outlier, kAlign);
@@ -1122,7 +1133,7 @@ qlin_status noalloc_scratch(unsigned** out) {
 // every tile is whole.
 struct BwdPlan {
   int ntk, tiles, full, tsplit;
-  size_t part_off, cnt_off, bytes;
+  size_t part_off, bytes;
 };
 
 BwdPlan plan_backward(int M, const qlin_weights* w, bool split) {
@@ -1137,7 +1148,7 @@ BwdPlan plan_backward(int M, const qlin_weights* w, bool split) {
   // only below two waves: with more, CTAs of different lengths already
   // interleave across the wave boundaries and the partials cost more than
   // the idle SMs of the last wave (measured on 3.5-wave grids)
-  if (split && tail > 0 && p.tiles < 2 * sms) {
+  if (split && tail > 0 && tail <= kHeadCounters && p.tiles < 2 * sms) {
     int S = sms / tail;
     if (S > 8) S = 8;
     if (S > nsteps) S = nsteps;
@@ -1147,9 +1158,8 @@ BwdPlan plan_backward(int M, const qlin_weights* w, bool split) {
     }
   }
   const int ntail = p.tiles - p.full;
-  p.part_off = 0;
-  p.cnt_off = round_up(size_t(ntail) * (p.tsplit - 1) * 65536 * 4, kAlign);
-  p.bytes = ntail ? round_up(p.cnt_off + size_t(ntail) * 4, kAlign) : 0;
+  p.part_off = sizeof(WorkspaceHead);
+  p.bytes = ntail ? round_up(p.part_off + size_t(ntail) * (p.tsplit - 1) * 65536 * 4, kAlign) : 0;
   return p;
 }
 
@@ -1238,10 +1248,11 @@ qlin_status forward_fused(const uint16_t* X, int32_t M, const qlin_weights* w, f
   int8_t* Xq = reinterpret_cast<int8_t*>(ws + L.xq);
   float* a = reinterpret_cast<float*>(ws + L.a);
   int8_t* XqO = nO > 0 ? reinterpret_cast<int8_t*>(ws + L.xqo) : nullptr;
-  char* gws = ws + L.gemm;
+  WorkspaceHead* head = head_of(workspace);
+  const GemmScratch gws{ws + L.gemm, head->cnt};
   const GemmPlan p = plan_gemm(M, w, true);
-  uint16_t* U = nO > 0 ? reinterpret_cast<uint16_t*>(gws + p.u_off[0]) : nullptr;
-  st = launch_quant(X, M, w, s, gamma, update, Xq, a, XqO, U, ws + L.act, stream);
+  uint16_t* U = nO > 0 ? reinterpret_cast<uint16_t*>(gws.p + p.u_off[0]) : nullptr;
+  st = launch_quant(X, M, w, s, gamma, update, Xq, a, XqO, U, head->cmax, head->momentum, stream);
   if (st != QLIN_OK) return st;
   return launch_gemm_fused(p, w, Xq, a, Y, gws, stream, epi, variant);
 }
@@ -1416,7 +1427,7 @@ struct FusedBwdLayout {
 FusedBwdLayout fused_bwd_layout(int M, const qlin_weights* w) {
   FusedBwdLayout L{};
   L.dx = plan_dx(M, w);
-  size_t off = 0;
+  size_t off = sizeof(WorkspaceHead);  // not used, left as it is
   L.wide = off; off = round_up(off + size_t((w->K + 127) / 128) * L.dx.nst * 16384, kAlign);
   L.dz = off; off = round_up(off + size_t(M) * w->N * 2, kAlign);
   L.rows = off; off = round_up(off + size_t(M) * 4, kAlign);
@@ -1616,7 +1627,7 @@ cudaError_t launch_norm_forward_ring(const RingPlan& p, unsigned grid, const Nor
 struct NormBwdLayout {
   RingPlan ring[2];  // without and with dres
   int G;             // row groups of the column kernel
-  size_t total;
+  size_t part, total;
 };
 NormBwdLayout norm_bwd_layout(int M, int K) {
   NormBwdLayout L{};
@@ -1627,7 +1638,8 @@ NormBwdLayout norm_bwd_layout(int M, int K) {
     const int n = static_cast<int>(ring_grid(L.ring[r], M));
     if (n > most) most = n;
   }
-  L.total = M > 0 ? round_up(size_t(2) * most * K * 4, kAlign) : 0;
+  L.part = sizeof(WorkspaceHead);  // the head is not used, left as it is
+  L.total = M > 0 ? round_up(L.part + size_t(2) * most * K * 4, kAlign) : 0;
   return L;
 }
 
@@ -1729,8 +1741,9 @@ qlin_status qlin_quant_act(const uint16_t* X, int32_t M, const qlin_weights* w, 
     return fail(QLIN_ERR_ALIGN, "an activation buffer is not 16-byte aligned");
   const size_t need = (update_momentum ? act_ws_bytes(w) : 0);
   if (ws_bytes < need || (need && !workspace)) return fail(QLIN_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
-  return launch_quant(X, M, w, s, gamma, update_momentum, Xq, a, XqO, nullptr, workspace,
-                      static_cast<cudaStream_t>(stream));
+  WorkspaceHead* head = head_of(workspace);
+  return launch_quant(X, M, w, s, gamma, update_momentum, Xq, a, XqO, nullptr, need ? head->cmax : nullptr,
+                      need ? head->momentum : nullptr, static_cast<cudaStream_t>(stream));
 }
 
 qlin_status qlin_quant_act_noalloc(const uint16_t* X, int32_t M, const qlin_weights* w, float* s, float gamma,
@@ -1758,7 +1771,8 @@ qlin_status qlin_quant_act_noalloc(const uint16_t* X, int32_t M, const qlin_weig
     // and the counter (they must start at zero) before this call uses them.
     QLIN_CUDA_TRY(cudaMemsetAsync(scratch, 0, (size_t(nO) + 1) * sizeof(unsigned), stream));
   }
-  return launch_quant(X, M, w, s, gamma, update_momentum, Xq, a, XqO, nullptr, scratch, stream);
+  return launch_quant(X, M, w, s, gamma, update_momentum, Xq, a, XqO, nullptr, scratch, scratch ? scratch + nO : nullptr,
+                      stream);
 }
 
 qlin_status qlin_outlier_colmax(const uint16_t* X, int32_t M, const qlin_weights* w, float* cmax, void* stream_) {
@@ -1795,7 +1809,8 @@ qlin_status qlin_gemm_workspace(int32_t M, const qlin_weights* w, size_t* bytes)
   qlin_status st = check_weights(w);
   if (st != QLIN_OK) return st;
   if (!bytes || M < 0) return fail(QLIN_ERR_ARG, "bad arguments");
-  *bytes = gemm_ws_bytes(M, w);
+  const size_t scratch = gemm_ws_bytes(M, w);
+  *bytes = scratch ? sizeof(WorkspaceHead) + scratch : 0;
   return QLIN_OK;
 }
 
@@ -1812,14 +1827,15 @@ qlin_status qlin_gemm(const qlin_weights* w, const int8_t* Xq, const float* a, c
   if (!aligned16(Xq) || !aligned16(a) || !aligned16(Y) || (acc_debug && !aligned16(acc_debug)) ||
       (XqO && !aligned16(XqO)) || (s && !aligned16(s)))
     return fail(QLIN_ERR_ALIGN, "a GEMM buffer is not 16-byte aligned");
-  const size_t need = gemm_ws_bytes(M, w);
+  const size_t scratch = gemm_ws_bytes(M, w), need = scratch ? sizeof(WorkspaceHead) + scratch : 0;
   if (ws_bytes < need || (need && !workspace)) return fail(QLIN_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
   if (need && reinterpret_cast<uintptr_t>(workspace) % kAlign)
     return fail(QLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  char* gws = static_cast<char*>(workspace);
+  GemmScratch gws{nullptr, nullptr};
+  if (need) gws = GemmScratch{static_cast<char*>(workspace) + sizeof(WorkspaceHead), head_of(workspace)->cnt};
   if (nO > 0) {
-    uint16_t* U = reinterpret_cast<uint16_t*>(gws + plan_gemm(M, w).u_off[0]);
+    uint16_t* U = reinterpret_cast<uint16_t*>(gws.p + plan_gemm(M, w).u_off[0]);
     const size_t total = size_t(M) * w->n_outlier_pad;
     comp_operand_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(XqO, s, M, nO,
                                                                                        w->n_outlier_pad, U);
@@ -1878,7 +1894,7 @@ qlin_status qlin_backward_dx(const qlin_weights* w, const uint16_t* dY, int32_t 
   args.full = p.full;
   args.tsplit = p.tsplit;
   args.part = p.bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_off) : nullptr;
-  args.cnt = p.bytes ? reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + p.cnt_off) : nullptr;
+  args.cnt = p.bytes ? head_of(workspace)->cnt : nullptr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   switch (w->fmt) {
     case QLIN_W4_PERCHANNEL: return launch_backward_t<kFmtW4PC>(tm, args, stream);
@@ -1914,10 +1930,11 @@ qlin_status qlin_forward(const uint16_t* X, int32_t M, const qlin_weights* w, fl
   int8_t* Xq = reinterpret_cast<int8_t*>(ws + L.xq);
   float* a = reinterpret_cast<float*>(ws + L.a);
   int8_t* XqO = nO > 0 ? reinterpret_cast<int8_t*>(ws + L.xqo) : nullptr;
-  char* gws = ws + L.gemm;
-  uint16_t* U = nO > 0 ? reinterpret_cast<uint16_t*>(gws + plan_gemm(M, w).u_off[0]) : nullptr;
+  WorkspaceHead* head = head_of(workspace);
+  const GemmScratch gws{ws + L.gemm, head->cnt};
+  uint16_t* U = nO > 0 ? reinterpret_cast<uint16_t*>(gws.p + plan_gemm(M, w).u_off[0]) : nullptr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  st = launch_quant(X, M, w, s, gamma, update_momentum, Xq, a, XqO, U, ws + L.act, stream);
+  st = launch_quant(X, M, w, s, gamma, update_momentum, Xq, a, XqO, U, head->cmax, head->momentum, stream);
   if (st != QLIN_OK) return st;
   return launch_gemm(w, Xq, a, M, Y, nullptr, gws, stream);
 }
@@ -2038,7 +2055,7 @@ qlin_status qlin_norm_backward(const uint16_t* dY, const uint16_t* X, int32_t M,
     if (ws_bytes < L.total || !workspace) return fail(QLIN_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, L.total);
     if (reinterpret_cast<uintptr_t>(workspace) % kAlign)
       return fail(QLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
-    g.part = static_cast<float*>(workspace);
+    g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.part);
   }
   if (ring.ctas > 0) {
     const unsigned grid = ring_grid(ring, M);
@@ -2103,7 +2120,8 @@ qlin_status qlin_forward_grouped(int32_t count, const qlin_weights* const* w, co
   if (ws_bytes < L.total || !workspace) return fail(QLIN_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, L.total);
   if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return fail(QLIN_ERR_ALIGN, "workspace must be 256-byte aligned");
   char* ws = static_cast<char*>(workspace);
-  char* gws = ws + L.gemm;
+  WorkspaceHead* head = head_of(workspace);
+  const GemmScratch gws{ws + L.gemm, head->cnt};
   QuantIO io[kMaxProbs];
   const int8_t* xq[kMaxProbs];
   const float* av[kMaxProbs];
@@ -2112,7 +2130,7 @@ qlin_status qlin_forward_grouped(int32_t count, const qlin_weights* const* w, co
     const bool o = w[q]->n_outlier > 0;
     io[q] = QuantIO{X[q], s[q], reinterpret_cast<int8_t*>(ws + L.xq[q]), reinterpret_cast<float*>(ws + L.a[q]),
                     o ? reinterpret_cast<int8_t*>(ws + L.xqo[q]) : nullptr,
-                    o ? reinterpret_cast<uint16_t*>(gws + L.plan.u_off[q]) : nullptr, ws + L.act[q]};
+                    o ? reinterpret_cast<uint16_t*>(gws.p + L.plan.u_off[q]) : nullptr, head->cmax, head->momentum + q};
     xq[q] = io[q].Xq;
     av[q] = io[q].a;
     yv[q] = Y[q];
@@ -2205,7 +2223,7 @@ qlin_status qlin_gptq_quantize(const double* X, int32_t ns, int32_t K, int32_t N
 
 namespace {
 struct SmoothLayout {
-  size_t cmax, wmax, xall, sv, xh, wh, packed, xq, a, gemm, y, acc, ref, total;
+  size_t cmax, wmax, xall, sv, xh, wh, packed, xq, a, cnt, gemm, y, acc, ref, total;
   Layout wl;
 };
 SmoothLayout smooth_layout(int M, int K, int N) {
@@ -2223,6 +2241,7 @@ SmoothLayout smooth_layout(int M, int K, int N) {
   L.a = off; off = round_up(off + size_t(M) * 4, kAlign);
   qlin_weights w{};
   w.K = K; w.N = N; w.fmt = QLIN_W4_PERCHANNEL; w.n_outlier = 0; w.n_outlier_pad = 0;
+  L.cnt = off; off = round_up(off + sizeof(WorkspaceHead::cnt), kAlign);
   L.gemm = off; off = round_up(off + gemm_ws_bytes(M, &w), kAlign);
   L.y = off; off = round_up(off + size_t(M) * N * 2, kAlign);
   L.acc = off; off = round_up(off + size_t(M) * N * 4, kAlign);
@@ -2273,7 +2292,7 @@ qlin_status qlin_smooth_search(const uint16_t* X, int32_t M, int32_t K, const ui
   st = qlin_weights_bind(&w, K, N, QLIN_W4_PERCHANNEL, 0, ws + L.packed, L.wl.total);
   if (st != QLIN_OK) return st;
   QLIN_CUDA_TRY(cudaMemsetAsync(cmax, 0, size_t(K) * 4, stream));
-  QLIN_CUDA_TRY(cudaMemsetAsync(ws + L.gemm, 0, L.y - L.gemm, stream));  // split-K counters start at zero
+  QLIN_CUDA_TRY(cudaMemsetAsync(ws + L.cnt, 0, sizeof(WorkspaceHead::cnt), stream));  // split-K counters start at zero
   QLIN_CUDA_TRY(cudaMemsetAsync(loss, 0, size_t(G) * 8, stream));
   smooth_colmax_kernel<<<dim3((K + 255) / 256, (M + 63) / 64), 256, 0, stream>>>(X, M, K, cmax);
   smooth_rowmax_kernel<<<K, 256, 0, stream>>>(W, N, wmax);
@@ -2288,9 +2307,9 @@ qlin_status qlin_smooth_search(const uint16_t* X, int32_t M, int32_t K, const ui
     // the layer's quantizers and integer product on the smoothed tensors
     st = qlin_pack_weights(Wh, nullptr, &w, stream);
     if (st != QLIN_OK) return st;
-    st = launch_quant(Xh, M, &w, nullptr, 0.f, 0, Xq, a, nullptr, nullptr, nullptr, stream);
+    st = launch_quant(Xh, M, &w, nullptr, 0.f, 0, Xq, a, nullptr, nullptr, nullptr, nullptr, stream);
     if (st != QLIN_OK) return st;
-    st = launch_gemm(&w, Xq, a, M, Y, acc, ws + L.gemm, stream);
+    st = launch_gemm(&w, Xq, a, M, Y, acc, GemmScratch{ws + L.gemm, reinterpret_cast<unsigned*>(ws + L.cnt)}, stream);
     if (st != QLIN_OK) return st;
     smooth_ref_kernel<<<dim3((N + kRefTile - 1) / kRefTile, (M + kRefTile - 1) / kRefTile), 256, 0, stream>>>(
         X, W, sv, M, K, N, ref);

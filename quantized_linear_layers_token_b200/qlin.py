@@ -30,6 +30,8 @@ QLIN_ACT_SILU = 4
 QLIN_NORM_LAYER = 0
 QLIN_NORM_RMS = 1
 
+QLIN_WORKSPACE_HEAD = 18688  # bytes that must be zero at the start of a workspace
+
 STATUS = {0: "QLIN_OK", 1: "QLIN_ERR_ARG", 2: "QLIN_ERR_SHAPE", 3: "QLIN_ERR_ALIGN",
           4: "QLIN_ERR_WORKSPACE", 5: "QLIN_ERR_CUDA", 6: "QLIN_ERR_TIMEOUT"}
 
@@ -513,7 +515,8 @@ def qlin_poll_device_status(stream=None):
 
 def empty_workspace(nbytes: int, device="cuda") -> torch.Tensor:
     """Zero-filled device buffer, 256-byte aligned (torch's allocator aligns
-    to 512 bytes), usable as any workspace."""
+    to 512 bytes), usable as any workspace, and by one call after another
+    whatever their layer, token count and entry point (include/qlin.h)."""
     return torch.zeros(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
