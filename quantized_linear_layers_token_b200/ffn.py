@@ -28,22 +28,66 @@ class Saved:
     s_down: torch.Tensor
 
 
+class Workspace:
+    """Device memory that the calls of one or of many blocks take turns on: one
+    buffer, as large as the largest call so far needed.  Calls on it run one
+    after the other on one stream, replays of captured calls among them.
+
+    A buffer that a captured call uses is kept for this object's life, so a
+    captured graph may be replayed as long as the object lives.  A capture
+    cannot enlarge the buffer for the calls outside it: a call that finds it too
+    small under a capture takes memory of its own in that graph.  So ``reserve``
+    the largest size (``GatedFeedForward.workspace_bytes``), or run such a call
+    once, before capturing.
+    """
+
+    def __init__(self, device: torch.device | str = "cuda"):
+        self.device = device
+        self._buf = None
+        self._captured = []   # buffers that captured calls use
+        self._of_graphs = []  # memory first made under a capture, one call's each
+
+    def _new(self, nbytes: int) -> torch.Tensor:
+        buf = torch.empty(max(nbytes, qlin.QLIN_WORKSPACE_HEAD), dtype=torch.uint8, device=self.device)
+        buf[:qlin.QLIN_WORKSPACE_HEAD].zero_()
+        return buf
+
+    def reserve(self, nbytes: int) -> None:
+        """Make the buffer at least this large (not under a capture)."""
+        if self._buf is None or self._buf.numel() < nbytes:
+            if self._buf is not None:
+                self._buf.record_stream(torch.cuda.current_stream(self._buf.device))  # its last call may still run
+            self._buf = self._new(nbytes)
+
+    def get(self, nbytes: int) -> torch.Tensor:
+        """A workspace of at least `nbytes` for the next call."""
+        if not torch.cuda.is_current_stream_capturing():
+            self.reserve(nbytes)
+        elif self._buf is None or self._buf.numel() < nbytes:
+            self._of_graphs.append(self._new(nbytes))  # its head zeroed by the graph, when it is replayed: for no other call
+            return self._of_graphs[-1]
+        elif not any(b is self._buf for b in self._captured):
+            self._captured.append(self._buf)
+        return self._buf
+
+
 class GatedFeedForward:
     """`gated` is packed by ``PackedLayer.pack_gated`` ([D] -> 2 [F]), `down`
     by ``PackedLayer.pack`` ([F] -> [D]).  gamma, beta and the biases are fp32
     (`bias_gated` in the packed order); beta and the biases may be None.
 
     A training forward updates both momentum states (`s_gated`, `s_down`) and
-    returns what its backward pass needs; several may be outstanding.  Calls of
-    one object run one after the other on one stream (they share workspaces),
-    replays of captured calls among them.  Workspaces change with the token
-    count; those that a captured call uses are kept for the object's life, so a
-    captured graph may be replayed as long as the object lives.
+    returns what its backward pass needs; several may be outstanding.  Calls run
+    one after the other on one stream (they share a workspace), replays of
+    captured calls among them.
+
+    The blocks of a model take turns on one `workspace`, which they are given
+    (by default each has its own: at 2048 tokens of LLaMA-2-70B's widths 1.2 GB).
     """
 
     def __init__(self, gated: qlin.PackedLayer, down: qlin.PackedLayer, gamma, beta=None, bias_gated=None,
                  bias_down=None, kind: int = qlin.QLIN_NORM_RMS, eps: float = 1e-5, act: int = qlin.QLIN_ACT_SILU,
-                 momentum: float = 0.9):
+                 momentum: float = 0.9, workspace: Workspace | None = None):
         if gated.K != down.N or gated.N != 2 * down.K:
             raise ValueError(f"gated [{gated.K}] -> [{gated.N}] and down [{down.K}] -> [{down.N}] do not fit together")
         self.gated, self.down = gated, down
@@ -53,26 +97,16 @@ class GatedFeedForward:
         dev = gated.buffer.device
         self.s_gated = torch.ones(gated.n_outlier, device=dev)
         self.s_down = torch.ones(down.n_outlier, device=dev)
-        self._ws = {}        # name -> (workspace, token count) of the last call
-        self._captured = {}  # (name, token count) -> workspace of captured calls
-        self._of_graphs = []  # workspaces first made under a capture, one call's each
+        self.workspace = Workspace(dev) if workspace is None else workspace
 
-    def _workspace(self, name: str, nbytes: int, M: int):
-        """A zero-filled buffer that belongs to one token count: what a call
-        leaves zero lies elsewhere at another count."""
-        ws = self._captured.get((name, M))
-        if ws is None:
-            capturing = torch.cuda.is_current_stream_capturing()
-            ws, n = self._ws.get(name, (None, -1))
-            if n != M or ws.numel() < nbytes:
-                ws = qlin.empty_workspace(nbytes, device=self.gated.buffer.device)
-                if capturing:  # zeroed by the graph that is being captured, when it is replayed: for no other call
-                    self._of_graphs.append(ws)
-                    return ws, nbytes
-                self._ws[name] = (ws, M)
-            if capturing:
-                self._captured[name, M] = ws
-        return ws, nbytes
+    def workspace_bytes(self, M: int, training: bool = False) -> int:
+        """What the workspace holds for a forward of M tokens; with `training`,
+        for its backward pass too."""
+        n = max(qlin.qlin_forward_gated_workspace(M, self.gated.w), qlin.qlin_forward_act_workspace(M, self.down.w))
+        if not training:
+            return n
+        return max(n, qlin.qlin_backward_act_workspace(M, self.down.w),
+                   qlin.qlin_backward_gated_workspace(M, self.gated.w), qlin.qlin_norm_backward_workspace(M, self.D))
 
     def _rows(self, t: torch.Tensor, name: str) -> int:
         if t.dim() != 2 or t.shape[1] != self.D:
@@ -91,10 +125,10 @@ class GatedFeedForward:
         mean = torch.empty(M, **f32) if training and self.kind == qlin.QLIN_NORM_LAYER else None
         rstd = torch.empty(M, **f32) if training else None
         qlin.qlin_norm_forward(x, M, self.D, self.kind, self.gamma, self.beta, self.eps, n, mean, rstd)
-        ws, nws = self._workspace("gated", qlin.qlin_forward_gated_workspace(M, self.gated.w), M)
+        ws = self.workspace.get(self.workspace_bytes(M))
+        nws = ws.numel()
         qlin.qlin_forward_gated(n, M, self.gated.w, self.s_gated, self.momentum, training, h, ws, nws, act=self.act,
                                 bias=self.bias_gated, Z=z)
-        ws, nws = self._workspace("down", qlin.qlin_forward_act_workspace(M, self.down.w), M)
         qlin.qlin_forward_act(h, M, self.down.w, self.s_down, self.momentum, training, y, ws, nws,
                               bias=self.bias_down, residual=x)
         if not training:
@@ -115,9 +149,8 @@ class GatedFeedForward:
 
         dbg, dbd = like(self.bias_gated, 2 * self.F), like(self.bias_down, self.D)
         dgamma, dbeta = like(self.gamma, self.D), like(self.beta, self.D)
-        nws = max(qlin.qlin_backward_act_workspace(M, self.down.w), qlin.qlin_backward_gated_workspace(M, self.gated.w),
-                  qlin.qlin_norm_backward_workspace(M, self.D))
-        ws, _ = self._workspace("backward", nws, M)
+        ws = self.workspace.get(self.workspace_bytes(M, training=True))
+        nws = ws.numel()
         qlin.qlin_backward_act(self.down.w, dy, None, M, saved.s_down, dh, dbd, ws, nws)
         qlin.qlin_backward_gated(self.gated.w, dh, saved.z, M, saved.s_gated, dn, dbg, ws, nws, act=self.act)
         qlin.qlin_norm_backward(dn, saved.x, M, self.D, self.kind, self.gamma, saved.mean, saved.rstd, dy, dx, dgamma,
