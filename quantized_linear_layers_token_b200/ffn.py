@@ -70,6 +70,13 @@ class Workspace:
             self._captured.append(self._buf)
         return self._buf
 
+    def reset(self) -> None:
+        """Ready again after a call gave up (QLIN_ERR_TIMEOUT): what has to be
+        zero at the start of each buffer is zero-filled, in place."""
+        for buf in [self._buf, *self._captured]:
+            if buf is not None:
+                buf[:qlin.QLIN_WORKSPACE_HEAD].zero_()
+
 
 class GatedFeedForward:
     """`gated` is packed by ``PackedLayer.pack_gated`` ([D] -> 2 [F]), `down`
@@ -83,6 +90,10 @@ class GatedFeedForward:
 
     The blocks of a model take turns on one `workspace`, which they are given
     (by default each has its own: at 2048 tokens of LLaMA-2-70B's widths 1.2 GB).
+
+    After QLIN_ERR_TIMEOUT (``qlin.qlin_poll_device_status``) the outputs of the
+    calls that gave up are undefined, and so is the `s_down` of a training
+    forward among them: call ``reset`` and put back the states of before.
     """
 
     def __init__(self, gated: qlin.PackedLayer, down: qlin.PackedLayer, gamma, beta=None, bias_gated=None,
@@ -107,6 +118,10 @@ class GatedFeedForward:
             return n
         return max(n, qlin.qlin_backward_act_workspace(M, self.down.w),
                    qlin.qlin_backward_gated_workspace(M, self.gated.w), qlin.qlin_norm_backward_workspace(M, self.D))
+
+    def reset(self) -> None:
+        """After a call gave up: the workspace is ready again (every block on it)."""
+        self.workspace.reset()
 
     def _rows(self, t: torch.Tensor, name: str) -> int:
         if t.dim() != 2 or t.shape[1] != self.D:

@@ -1,5 +1,6 @@
 """The feed-forward block's workspace: shared by the blocks of a model, grown
-by token counts and captures in any order.  Every result is that of a block of its own."""
+by token counts and captures in any order, and made ready again after a
+bounded wait gave up.  Every result is that of a block of its own."""
 import pytest
 import torch
 
@@ -77,6 +78,45 @@ def test_captures_around_a_growing_buffer(q, oracle):  # noqa: F811
         assert equal(out, want), k
         assert torch.equal(b.ffn.forward(x), own.ffn.forward(x))
     del junk
+    q.qlin_poll_device_status()
+
+
+def test_reset_after_a_wait_gave_up(q, oracle):  # noqa: F811
+    """Waits without time give up; after reset() every token count is right
+    again, eagerly and in a graph captured before, whatever the workspace holds."""
+    D, F = 16384, 1024
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda").half()  # noqa: E731
+    import numpy as np
+    from quantized_linear_layers_token_b200.ffn import GatedFeedForward
+    O = np.arange(9, dtype=np.int32) * 5
+    gated = q.PackedLayer.pack_gated(n(D, F) * 0.02, n(D, F) * 0.02, O, synth.W8_PERCHANNEL)
+    down = q.PackedLayer.pack(n(F, D) * 0.02, O, synth.W8_PERCHANNEL)
+    gamma = torch.ones(D, device="cuda")
+    make = lambda: GatedFeedForward(gated, down, gamma)  # noqa: E731
+    block = make()
+    xs = {M: n(M, D) for M in (1, 16, 40, 90, 300, 600)}
+    want = {M: step(make(), x, x) for M, x in xs.items()}
+    q.qlin_poll_device_status()
+    block.workspace.reserve(block.workspace_bytes(600, training=True))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(block, xs[16], xs[16])
+    keep = block.s_gated.clone(), block.s_down.clone()
+    with q.knobs(wait_ns=0):
+        block.forward(xs[600], training=True)
+        with pytest.raises(q.QlinError) as e:
+            q.qlin_poll_device_status()
+        assert q.STATUS[e.value.status] == "QLIN_ERR_TIMEOUT"
+    block.s_gated.copy_(keep[0])
+    block.s_down.copy_(keep[1])
+    block.workspace.get(1).fill_(255)  # whatever state such a call may leave
+    block.reset()
+    for M in (600, 16, 1, 300, 90, 40):
+        assert equal(step(block, xs[M], xs[M]), want[M]), M
+    graph.replay()
+    assert equal(out, want[16])
     q.qlin_poll_device_status()
 
 
