@@ -8,10 +8,13 @@ rank the global maxima; each rank then applies the recurrence itself
 (qlin_momentum_update), so all replicas keep the same state s.  The maximum
 is exact and order-free, so the result is bit-identical to the update over
 the unsharded batch.
+
+A layer whose input depends on other layers' scales (the second half of a
+feed-forward block) is reduced on its own, by `max_over_ranks`.
 """
 from __future__ import annotations
 
-from typing import Sequence
+from typing import Callable, Sequence
 
 import torch
 
@@ -45,3 +48,16 @@ class ColmaxExchange:
         import torch.distributed as dist
         if dist.is_available() and dist.is_initialized() and dist.get_world_size(group) > 1:
             dist.all_reduce(self.buf, op=dist.ReduceOp.MAX, group=group)
+
+
+def max_over_ranks(group=None) -> Callable[[torch.Tensor], None]:
+    """The reduction that ``ffn.GatedFeedForward`` takes as `reduce_max`: one
+    all-reduce(MAX), in place, of a layer's column maxima (collective: all ranks
+    call it in the same order each step)."""
+
+    def reduce(cmax: torch.Tensor) -> None:
+        import torch.distributed as dist
+        if dist.is_available() and dist.is_initialized() and dist.get_world_size(group) > 1:
+            dist.all_reduce(cmax, op=dist.ReduceOp.MAX, group=group)
+
+    return reduce

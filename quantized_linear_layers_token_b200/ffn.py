@@ -11,6 +11,7 @@ holds the memory and nothing else.
 from __future__ import annotations
 
 from dataclasses import dataclass
+from typing import Callable
 
 import torch
 
@@ -91,6 +92,15 @@ class GatedFeedForward:
     The blocks of a model take turns on one `workspace`, which they are given
     (by default each has its own: at 2048 tokens of LLaMA-2-70B's widths 1.2 GB).
 
+    Data-parallel training: every rank's scales have to come from all ranks'
+    tokens, or the replicas' states drift apart.  `reduce_max` combines a rank's
+    fp32 vector of outlier column maxima with the other ranks' in place
+    (``dp.max_over_ranks``); a training forward then calls it before each of its
+    two quantizations, on every rank in the same order, a rank without tokens
+    among them, and updates both states from the result, the same on every rank:
+    the update over the unsharded batch.  Without it the states follow this
+    process's tokens alone.
+
     After QLIN_ERR_TIMEOUT (``qlin.qlin_poll_device_status``) the outputs of the
     calls that gave up are undefined, and so is the `s_down` of a training
     forward among them: call ``reset`` and put back the states of before.
@@ -98,7 +108,8 @@ class GatedFeedForward:
 
     def __init__(self, gated: qlin.PackedLayer, down: qlin.PackedLayer, gamma, beta=None, bias_gated=None,
                  bias_down=None, kind: int = qlin.QLIN_NORM_RMS, eps: float = 1e-5, act: int = qlin.QLIN_ACT_SILU,
-                 momentum: float = 0.9, workspace: Workspace | None = None):
+                 momentum: float = 0.9, workspace: Workspace | None = None,
+                 reduce_max: Callable[[torch.Tensor], None] | None = None):
         if gated.K != down.N or gated.N != 2 * down.K:
             raise ValueError(f"gated [{gated.K}] -> [{gated.N}] and down [{down.K}] -> [{down.N}] do not fit together")
         self.gated, self.down = gated, down
@@ -109,15 +120,17 @@ class GatedFeedForward:
         self.s_gated = torch.ones(gated.n_outlier, device=dev)
         self.s_down = torch.ones(down.n_outlier, device=dev)
         self.workspace = Workspace(dev) if workspace is None else workspace
+        self.reduce_max = reduce_max
 
     def workspace_bytes(self, M: int, training: bool = False) -> int:
         """What the workspace holds for a forward of M tokens; with `training`,
         for its backward pass too."""
         n = max(qlin.qlin_forward_gated_workspace(M, self.gated.w), qlin.qlin_forward_act_workspace(M, self.down.w))
-        if not training:
-            return n
-        return max(n, qlin.qlin_backward_act_workspace(M, self.down.w),
-                   qlin.qlin_backward_gated_workspace(M, self.gated.w), qlin.qlin_norm_backward_workspace(M, self.D))
+        return max(n, self._backward_bytes(M)) if training else n
+
+    def _backward_bytes(self, M: int) -> int:
+        return max(qlin.qlin_backward_act_workspace(M, self.down.w), qlin.qlin_backward_gated_workspace(M, self.gated.w),
+                   qlin.qlin_norm_backward_workspace(M, self.D))
 
     def reset(self) -> None:
         """After a call gave up: the workspace is ready again (every block on it)."""
@@ -131,6 +144,18 @@ class GatedFeedForward:
     def _half(self, *shape):
         return torch.empty(shape, dtype=torch.float16, device=self.gated.buffer.device)
 
+    def _update(self, x: torch.Tensor, M: int, layer: qlin.PackedLayer, s: torch.Tensor) -> bool:
+        """Whether the layer's own call is to update its momentum state from
+        its input x; with `reduce_max` it is done here, from all ranks' maxima."""
+        if self.reduce_max is None:
+            return True
+        if layer.n_outlier > 0:
+            cmax = torch.empty(layer.n_outlier, dtype=torch.float32, device=s.device)
+            qlin.qlin_outlier_colmax(x, M, layer.w, cmax)
+            self.reduce_max(cmax)
+            qlin.qlin_momentum_update(layer.w, cmax, s, self.momentum)
+        return False
+
     def forward(self, x: torch.Tensor, training: bool = False):
         """y [M][D] of x fp16 [M][D]; with `training`, (y, Saved)."""
         M = self._rows(x, "x")
@@ -142,9 +167,11 @@ class GatedFeedForward:
         qlin.qlin_norm_forward(x, M, self.D, self.kind, self.gamma, self.beta, self.eps, n, mean, rstd)
         ws = self.workspace.get(self.workspace_bytes(M))
         nws = ws.numel()
-        qlin.qlin_forward_gated(n, M, self.gated.w, self.s_gated, self.momentum, training, h, ws, nws, act=self.act,
+        update = training and self._update(n, M, self.gated, self.s_gated)
+        qlin.qlin_forward_gated(n, M, self.gated.w, self.s_gated, self.momentum, update, h, ws, nws, act=self.act,
                                 bias=self.bias_gated, Z=z)
-        qlin.qlin_forward_act(h, M, self.down.w, self.s_down, self.momentum, training, y, ws, nws,
+        update = training and self._update(h, M, self.down, self.s_down)
+        qlin.qlin_forward_act(h, M, self.down.w, self.s_down, self.momentum, update, y, ws, nws,
                               bias=self.bias_down, residual=x)
         if not training:
             return y
@@ -164,7 +191,7 @@ class GatedFeedForward:
 
         dbg, dbd = like(self.bias_gated, 2 * self.F), like(self.bias_down, self.D)
         dgamma, dbeta = like(self.gamma, self.D), like(self.beta, self.D)
-        ws = self.workspace.get(self.workspace_bytes(M, training=True))
+        ws = self.workspace.get(self._backward_bytes(M))
         nws = ws.numel()
         qlin.qlin_backward_act(self.down.w, dy, None, M, saved.s_down, dh, dbd, ws, nws)
         qlin.qlin_backward_gated(self.gated.w, dh, saved.z, M, saved.s_gated, dn, dbg, ws, nws, act=self.act)
