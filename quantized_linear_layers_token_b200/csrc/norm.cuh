@@ -20,8 +20,6 @@
 
 namespace qlin {
 
-constexpr int kNormMaxVec = 8192;  // 8-element vectors of a row (K <= 65536)
-
 struct NormFwdArgs {
   const uint16_t* X;   // [M][K]
   const float* gamma;  // [K]
