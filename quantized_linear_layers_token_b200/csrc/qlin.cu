@@ -436,10 +436,14 @@ GemmPlan plan_gemm_group(int M, const qlin_weights* const* ws, int n, bool fused
   off = round_up(off + (p.split ? size_t(2) * p.grid * slot_bytes : 0), kAlign);
   p.comp_off = off;
   off = round_up(off + (p.split && any_outliers ? size_t(2) * p.grid * slot_bytes : 0), kAlign);
-  // A fused launch widens from its second token tile on (10 to 15 % faster at
-  // 257 to 511 tokens), except where widening a very large per-channel layer
-  // costs more than it gives (8192 -> 28672 at 300 tokens: 187 against 165 us);
-  // and in its first tile of 256 while the layer is small for the tokens (4096
+  // A fused launch widens from its second token tile on.  g128 layers gain at
+  // every size measured (at 257 tokens 4096 -> 11008 41 against 54 us, 4096 ->
+  // 2 x 11008 70 against 75, 8192 -> 2 x 28672 299 against 310).  Per-channel ones,
+  // whose codes cost less to convert inside the kernel, gain where they are small
+  // (4096 -> 4096 24 against 28, 4096 -> 11008 41 against 45) and lose towards the
+  // limit below (4096 -> 2 x 11008 69.5 against 61 at 257 tokens, 84 against 80 at
+  // 700); past it they widen as other launches do.  And in the first tile of 256
+  // while the layer is small for the tokens (4096
   // -> 4096 at 129 tokens 25.3 against 28.3 us, at 256 25.4 against 33.5; 1024
   // -> 1024 14 against 17 and 21; but 4096 -> 11008 at 129 36 against 30).
   int widen_from = widen_min_m();
