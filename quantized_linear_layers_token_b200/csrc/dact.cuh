@@ -226,10 +226,12 @@ __global__ void __launch_bounds__(128) dact_columns_kernel(const __grid_constant
 // the mantissas of the channel factors stay in registers where they fit
 // beside the column sums, which ACC keeps over the CTA's rows and writes once
 // as partial row blockIdx.x.  dZ is skipped when it is null (only the bias's
-// gradient is wanted).  The slopes' arithmetic and the latency of a row's one
-// barrier bound it before HBM does: 2048 x 11008, GELU (tanh), 38 us = 3.6
-// TB/s; gated 2048 x 22016, SiLU, 47 us = 4.8 TB/s.  Two rows at a time gave
-// nothing.
+// gradient is wanted).  2048 x 11008, GELU (tanh), 38 us = 3.6 TB/s; gated 2048 x
+// 22016, SiLU, 47 us = 4.8 TB/s.  Nothing is saturated (first case: issue slots
+// half used, DRAM a third): with one CTA of 22 warps an SM, what a warp waits
+// for is spread over dependent arithmetic, shared memory and the special
+// functions, the row's barrier (an eighth) and the next row.  Two rows at a time
+// gave nothing, nor did two CTAs of half the threads (41 us).
 template <bool GATED, int VPT, bool ACC>
 __global__ void __launch_bounds__(kDactRingThreads) dact_ring_kernel(const __grid_constant__ DactArgs g) {
   constexpr bool kKeep = VPT * (ACC ? 2 : 1) <= 4;

@@ -78,7 +78,9 @@ struct DxWidenArgs {
 // by two threads a row, and one bulk copy each takes them out.  The column
 // sums of the bias's gradient ride along in CTAs of their own: alone they are
 // a launch that waits for a few loads.  4096 x 11008 INT8: 33 us, 4.1 TB/s of
-// codes and operand; 4096 x 22016 g128: 49 us, 4.6 TB/s.
+// codes and operand; 4096 x 22016 g128: 49 us, 4.6 TB/s.  A warp waits for
+// its codes two fifths of the time: a CTA loads, converts and stores in turn, and
+// five of them on an SM do not cover it.
 template <int FMT>
 __global__ void __launch_bounds__(256) dx_widen_kernel(const __grid_constant__ DxWidenArgs g) {
   __shared__ __align__(128) unsigned char blk[32768];
