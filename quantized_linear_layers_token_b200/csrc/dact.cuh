@@ -288,10 +288,11 @@ __global__ void __launch_bounds__(kDactRingThreads) dact_ring_kernel(const __gri
   }
   // the usual case: every channel factor's mantissa is its fraction field
   if (!kKeep) inside = __syncthreads_and(inside);
+  bool ok = true;  // a thread whose wait gave up waits no more: what follows it is not used
   int i = 0;
   for (size_t m = blockIdx.x; m < M; m += step, ++i) {
     const int s = i % S;
-    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) abort_flag = 1;
+    if (ok && !mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) ok = false;
     const uint4* zr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
     const unsigned char* yr = ring_smem + s * stage + zb;
     auto values = [&](int v, uint4& z, uint4& y) {

@@ -344,12 +344,13 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const __grid_con
     }
   }
   const float invk = 1.f / static_cast<float>(g.K);
+  bool ok = true;  // a thread whose wait gave up waits no more: what follows it is not used
   int i = 0;
   for (size_t grp = blockIdx.x; grp < groups; grp += step, ++i) {
     const int s = i % S;
     const int rows = group_rows(grp, R, g.M);
     const size_t m0 = grp * R;
-    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) abort_flag = 1;
+    if (ok && !mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) ok = false;
     const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
     f32x2 x[R][VPT][4];  // the rows' values, then x - mu
     float mu[R], q[R];
@@ -478,6 +479,7 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_co
     }
   };
   statistics(blockIdx.x);
+  bool ok = true;  // a thread whose wait gave up waits no more: what follows it is not used
   int i = 0;
   for (size_t grp = blockIdx.x; grp < groups; grp += step, ++i) {
     const int s = i % S;
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(const __grid_co
       rs[r] = rs1[r];
     }
     statistics(grp + step);
-    if (!mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) abort_flag = 1;
+    if (ok && !mbar_wait(&full[s], static_cast<uint32_t>(i / S) & 1u, &abort_flag)) ok = false;
     const uint4* dr = reinterpret_cast<const uint4*>(ring_smem + s * stage);
     const uint4* xr = reinterpret_cast<const uint4*>(ring_smem + s * stage + part);
     const uint4* rr = reinterpret_cast<const uint4*>(ring_smem + s * stage + 2 * part);
