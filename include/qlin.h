@@ -362,9 +362,9 @@ QLIN_API qlin_status qlin_forward_act(const uint16_t* X, int32_t M, const qlin_w
  *   workspace  qlin_backward_act_workspace bytes, 256-byte aligned; no
  *          zero-fill needed, and its first QLIN_WORKSPACE_HEAD bytes are left
  *          as they are.
- * Arithmetic: dZ is formed in fp32 and rounded to fp16 once, multiplied by
- * the mantissa of c'_n and by a power of two of its row that keeps it in
- * range whatever the gradients' scale; the outlier rows of Weff are rounded
+ * Arithmetic: dZ is formed in fp32 and rounded to fp16 once (up to 128 tokens
+ * carried as two fp16 terms), multiplied by the mantissa of c'_n and by a power
+ * of two of its row that keeps it in range whatever the gradients' scale; the outlier rows of Weff are rounded
  * to fp16, the other operand is exact; products are summed in fp32 and dX is
  * rounded once.  dbias sums the fp32 dZ in an order fixed by the shape.
  * M = 0 writes zeros to dbias; M above 65535 * 128 returns QLIN_ERR_SHAPE. */

@@ -7,7 +7,8 @@
 //           dZ[m][2j + 1] = dY[m][j] act(Z[m][2j])
 //   dbias_n = sum_m dZ[m][n]
 //
-// The product runs on the fp16 tensor cores, so dZ is rounded to fp16 once.
+// The product runs on the fp16 tensor cores, so dZ is rounded to fp16 once, or
+// carried as two fp16 terms where the product has rows to spare (dx_pair.cuh).
 // It is written as dZ m_n 2^(e_m) (dx_pair.cuh: m_n the mantissa of the
 // channel scale): the power of two of each row puts the largest |dZ| the row
 // can hold near 2^14, so neither a large gradient times a large up value
@@ -28,11 +29,12 @@ struct DactArgs {
   const uint16_t* dY;   // [M][N], gated: [M][N / 2]
   const uint16_t* Z;    // [M][N], or null when act is kActNone (never read then)
   const float* cscale;  // c_n [N]
-  uint16_t* dZ;         // [M][N] scaled (rows kernel)
-  float* rowscale;      // [M] 2^-e_m (rows kernel)
+  uint16_t* dZ;         // [M][N] scaled; two terms: [2 M][N], what a row's rounding left in the row behind it
+  float* rowscale;      // [M] 2^-e_m
   float* part;          // [G][N] partial column sums (columns kernel)
   float cmul;           // c'_n / c_n
   int M, N, act, G;
+  int two;              // dZ in two terms
   int stages;           // ring kernel
 };
 
@@ -67,12 +69,23 @@ __device__ __forceinline__ void dact_vec(int act, const uint4 zv, const uint4 yv
   }
 }
 
-// dZ m_n 2^e of the channels of vector v in fp16.
-__device__ __forceinline__ uint4 dact_scaled(const f32x2 (&d)[4], float scale, const f32x2 (&mant)[4]) {
+// dZ m_n 2^e of the channels of vector v of row m, written in one fp16 term or
+// in two (the second is the rest that the first left, rounded).
+__device__ __forceinline__ void dact_store(const DactArgs& g, size_t m, int v, const f32x2 (&d)[4], float scale,
+                                           const f32x2 (&mant)[4]) {
   f32x2 o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = f2_mul(f2_mul(d[i], f2_both(scale)), mant[i]);
-  return f2_to_h8(o);
+  const uint4 hi = f2_to_h8(o);
+  uint16_t* row = g.dZ + (g.two ? 2 * m : m) * g.N;
+  reinterpret_cast<uint4*>(row)[v] = hi;
+  if (g.two) {
+    f32x2 h[4];
+    h8_to_f2(hi, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f2_fma(h[i], f2_both(-1.f), o[i]);
+    reinterpret_cast<uint4*>(row + g.N)[v] = f2_to_h8(o);
+  }
 }
 __device__ __forceinline__ void load_mant(const DactArgs& g, int v, f32x2 (&m)[4]) {
   float c[8];
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(kDactThreads) dact_rows_kernel(const __grid_co
       dact_load<GATED>(g, m, v, z, y);
       dact_vec<GATED, kLimits>(g.act, z, y, d);
       load_mant(g, v, c);
-      reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, c);
+      dact_store(g, m, v, d, scale, c);
     }
     return true;
   };
@@ -338,7 +351,7 @@ __global__ void __launch_bounds__(kDactRingThreads) dact_ring_kernel(const __gri
               if (inside) load_fraction(g, v, c);
               else load_mant(g, v, c);
             }
-            reinterpret_cast<uint4*>(g.dZ + m * g.N)[v] = dact_scaled(d, scale, kKeep ? mant[kKeep ? j : 0] : c);
+            dact_store(g, m, v, d, scale, kKeep ? mant[kKeep ? j : 0] : c);
           }
         }
       }

@@ -7,6 +7,13 @@
 // blended outlier rows (p_n B + (s - 1) W_O / m_n) / s, rounded once.  So
 // the roundings are those of dZ, of the outlier rows and of dX.
 //
+// Up to 128 tokens, which would leave half of a tile's rows empty, dZ arrives in
+// two fp16 terms instead: rows 2m and 2m + 1 of the product are token m's value
+// and what its rounding left, and the epilogue adds the two lanes.  With few
+// tokens the gradient has few numbers, and the rounding of dZ alone took its
+// error to as much as twice that of one rounding of dX (1.42 times at the
+// median); with two terms the last rounding is all that counts.
+//
 // Widening once (dx_widen_kernel, bound by HBM: 2 K N bytes written) and
 // reading fp16 blocks by TMA leaves the tensor cores of both kernels' tiles
 // to the product.  Converting inside the product, one code block per 256
@@ -187,14 +194,15 @@ struct DxArgs {
   uint16_t* dX;           // [M][K] (reduce kernel)
   float* part;            // [S][M][K] partial sums (S > 1)
   int M, K;
+  int two;                // dZ in two terms (M <= 128)
   int nst;                // 64-channel steps of the whole reduction
   int tiles_k, tiles_m, S, units, ncl, gm;
 };
 
 struct alignas(64) DxParams {
-  CUtensorMap tmA;  // scaled dZ fp16 [M][N], 64 x 128 boxes, 128-byte swizzle
+  CUtensorMap tmA;  // scaled dZ fp16 [M][N] (two terms: [2 M][N]), 64 x 128 boxes, 128-byte swizzle
   CUtensorMap tmB;  // operand blocks as rows of 128 bytes, 128 rows a block
-  CUtensorMap tmX;  // dX fp16 [M][K], 64 x 128 boxes, 128-byte swizzle (stores)
+  CUtensorMap tmX;  // dX fp16 [M][K], 64 x 128 boxes (two terms: 64 x 64), 128-byte swizzle (stores)
   DxArgs g;
 };
 
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(DxCfg::kThreads, 1) dx_pair_kernel(const __gri
       bool ok = true;
       for (int u = cid; ok && u < g.units; u += g.ncl) {
         const DxUnit w = dx_unit(g, u);
-        const int m0 = w.tm * 256 + crk * 128;               // this CTA's 128 tokens
+        const int m0 = w.tm * 256 + crk * 128;               // this CTA's 128 rows of dZ
         const int b0 = (2 * w.tk + crk) * g.nst;             // this CTA's 128 inputs
         for (int j = w.j0; j < w.j1; ++j, ++gi) {
           const int s = gi % S;
@@ -371,6 +379,8 @@ __global__ void __launch_bounds__(DxCfg::kThreads, 1) dx_pair_kernel(const __gri
     const int grp = ep >> 2;
     const int quad = warp & 3;  // TMEM lanes 32*quad .. +31
     const int row = quad * 32 + lane;
+    const int trow = g.two ? row >> 1 : row;     // its token among the CTA's, which its even lane writes
+    const bool mine = !g.two || !(lane & 1);
     const bool issuer = ep == 0 && lane == 0;
     griddep_wait();  // the rows' factors come from a previous kernel
     int ti = 0;
@@ -378,18 +388,18 @@ __global__ void __launch_bounds__(DxCfg::kThreads, 1) dx_pair_kernel(const __gri
     for (int u = cid; u < g.units; u += g.ncl, ++ti) {
       const DxUnit w = dx_unit(g, u);
       const int buf = ti & 1;
-      const int m0 = w.tm * 256 + crk * 128;
-      const int m = m0 + row;
+      const int m0 = g.two ? crk * 64 : w.tm * 256 + crk * 128;
+      const int m = m0 + trow;
       const int k0 = w.tk * 256;
       const uint32_t lempty = mapa_shared(smem_u32(&acc_empty[buf]), 0);
       const float f = m < g.M && g.S == 1 ? g.rowscale[m] : 1.f;
       if (ok) ok = mbar_wait(&acc_full[buf], static_cast<uint32_t>(ti >> 1) & 1u, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(buf * 256);
+      const uint32_t tacc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(buf * 256);
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
-        unsigned char* yb = smem + C::kOffY + c * C::kChunk + grp * 16384 + row * 128;
+        unsigned char* yb = smem + C::kOffY + c * C::kChunk + grp * 16384 + trow * 128;
         if (g.S == 1) {
           if (issuer) bulk_wait_group_read1();  // the store of this chunk's previous contents has read them
           named_bar_sync(1, 256);
@@ -401,11 +411,16 @@ __global__ void __launch_bounds__(DxCfg::kThreads, 1) dx_pair_kernel(const __gri
 #pragma unroll
           for (int j = 0; j < 16; ++j) r[j] = 0u;
           if (ok) {
-            tmem_ld16(trow + col, r);
+            tmem_ld16(tacc + col, r);
             tmem_ld_wait();
           }
+          if (g.two) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(__shfl_xor_sync(0xffffffffu, r[j], 1)));
+          }
           if (g.S > 1) {
-            if (m < g.M && k0 + col < g.K) {  // K % 32 == 0: sixteen inputs or none
+            if (mine && m < g.M && k0 + col < g.K) {  // K % 32 == 0: sixteen inputs or none
               float4* dst = reinterpret_cast<float4*>(g.part + (static_cast<size_t>(w.sp) * g.M + m) * g.K + k0 + col);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -418,8 +433,10 @@ __global__ void __launch_bounds__(DxCfg::kThreads, 1) dx_pair_kernel(const __gri
             for (int e = 0; e < 8; ++e)
               hw[e] = h2_as_u32(__floats2half2_rn(__fmul_rn(__uint_as_float(r[2 * e]), f),
                                                   __fmul_rn(__uint_as_float(r[2 * e + 1]), f)));
-            *reinterpret_cast<uint4*>(yb + (((2 * q) ^ (row & 7)) << 4)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-            *reinterpret_cast<uint4*>(yb + (((2 * q + 1) ^ (row & 7)) << 4)) = make_uint4(hw[4], hw[5], hw[6], hw[7]);
+            if (mine) {
+              *reinterpret_cast<uint4*>(yb + (((2 * q) ^ (trow & 7)) << 4)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+              *reinterpret_cast<uint4*>(yb + (((2 * q + 1) ^ (trow & 7)) << 4)) = make_uint4(hw[4], hw[5], hw[6], hw[7]);
+            }
           }
         }
         if (c == 1) {

@@ -1287,6 +1287,7 @@ qlin_status launch_column_sum(const float* part, int G, int K, float* out0, floa
 // more for its pipeline's ends, a split the traffic of its partial sums.
 struct DxPlan {
   int tiles_k, tiles_m, S, units, ncl, nst, gm;
+  int two;  // dZ in two fp16 terms: both fit in one tile's rows
 };
 
 int dx_max_clusters() {
@@ -1322,6 +1323,7 @@ int dx_max_clusters() {
 DxPlan plan_dx(int M, const qlin_weights* w) {
   DxPlan p{};
   const int pairs = dx_max_clusters() > 0 ? dx_max_clusters() : 1;
+  p.two = M <= 128 ? 1 : 0;
   p.tiles_k = (w->K + 255) / 256;
   p.tiles_m = (M + 255) / 256;
   p.nst = (w->N + 63) / 64;
@@ -1433,7 +1435,7 @@ FusedBwdLayout fused_bwd_layout(int M, const qlin_weights* w) {
   L.dx = plan_dx(M, w);
   size_t off = sizeof(WorkspaceHead);  // not used, left as it is
   L.wide = off; off = round_up(off + size_t((w->K + 127) / 128) * L.dx.nst * 16384, kAlign);
-  L.dz = off; off = round_up(off + size_t(M) * w->N * 2, kAlign);
+  L.dz = off; off = round_up(off + size_t(L.dx.two ? 2 : 1) * M * w->N * 2, kAlign);
   L.rows = off; off = round_up(off + size_t(M) * 4, kAlign);
   L.dxpart = off; off = round_up(off + (L.dx.S > 1 ? size_t(L.dx.S) * M * w->K * 4 : 0), kAlign);
   // partial rows of the bias's gradient: one per CTA of a ring kernel (whose
@@ -1489,12 +1491,14 @@ qlin_status launch_dx(const qlin_weights* w, int M, const FusedBwdLayout& L, cha
   g.units = p.units;
   g.ncl = p.ncl;
   g.gm = p.gm;
-  st = make_map(&prm.tmA, ws + L.dz, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->N, M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  g.two = p.two;
+  st = make_map(&prm.tmA, ws + L.dz, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->N, static_cast<uint64_t>(p.two ? 2 : 1) * M, 64,
+                128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != QLIN_OK) return st;
   st = make_map(&prm.tmB, ws + L.wide, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, kb * p.nst * 128, 128, 128,
                 CU_TENSOR_MAP_SWIZZLE_NONE);
   if (st != QLIN_OK) return st;
-  st = make_map(&prm.tmX, dX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->K, M, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  st = make_map(&prm.tmX, dX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w->K, M, 64, p.two ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != QLIN_OK) return st;
   cudaError_t e = allow_smem<dx_pair_kernel>(DxCfg::kSmem);
   if (e != cudaSuccess) return fail(QLIN_ERR_CUDA, "dx_pair_kernel attribute: %s", cudaGetErrorString(e));
@@ -1542,6 +1546,7 @@ qlin_status backward_fused(const qlin_weights* w, const uint16_t* dY, const uint
   g.Z = Z;
   g.cscale = w->chan_scale;
   g.dZ = reinterpret_cast<uint16_t*>(ws + L.dz);
+  g.two = L.dx.two;
   g.rowscale = reinterpret_cast<float*>(ws + L.rows);
   g.part = reinterpret_cast<float*>(ws + L.part);
   g.cmul = w->fmt == QLIN_W4_PERCHANNEL ? 0.0625f : 1.f;
