@@ -1055,8 +1055,8 @@ FwdLayout forward_layout(int M, const qlin_weights* w, bool fused = false) {
   return L;
 }
 
-// Workspace of a grouped forward: the head, per problem Xq, a and XqO, then the GEMM launch's scratch (every problem's U and the
-// shared split-K slots and counters).
+// Workspace of a grouped forward: the head, per problem Xq, a and XqO, then
+// the GEMM launch's scratch (every problem's U and the shared split-K slots).
 struct GroupLayout {
   size_t xq[kMaxProbs], a[kMaxProbs], xqo[kMaxProbs];
   size_t gemm, total;
