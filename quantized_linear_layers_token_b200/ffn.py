@@ -56,6 +56,8 @@ class Workspace:
     def reserve(self, nbytes: int) -> None:
         """Make the buffer at least this large (not under a capture)."""
         if self._buf is None or self._buf.numel() < nbytes:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a workspace cannot be enlarged under a capture: reserve it before")
             if self._buf is not None:
                 self._buf.record_stream(torch.cuda.current_stream(self._buf.device))  # its last call may still run
             self._buf = self._new(nbytes)

@@ -141,3 +141,21 @@ def test_memory_of_a_large_block(q):  # noqa: F811
     assert used == [blocks[0].workspace_bytes(M, training=True)] * 2
     assert used[0] == max(q.qlin_forward_gated_workspace(M, gated.w), q.qlin_forward_act_workspace(M, down.w),
                           q.qlin_backward_act_workspace(M, down.w), q.qlin_backward_gated_workspace(M, gated.w))
+
+
+def test_reserve_under_a_capture_is_refused(q):  # noqa: F811
+    """The graph's memory would be taken for the buffer of every later call."""
+    from quantized_linear_layers_token_b200.ffn import Workspace
+    ws = Workspace()
+    ws.reserve(1 << 16)
+    x = torch.zeros(8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.add_(1)
+        ws.reserve(1 << 10)  # large enough: nothing to do
+        with pytest.raises(RuntimeError):
+            ws.reserve(1 << 20)
+    assert ws._buf.numel() == 1 << 16 and not ws._of_graphs
+    g.replay()
+    assert (x == 1).all()
